@@ -286,7 +286,7 @@ def run(s):
     if c["kind"] == "xattn_bwd":
         return _attend_bwd(s)
     x = s["x"].float()
-    sx = x.abs().amax(1, keepdim=True) / 127
+    sx = (x.abs().amax(1, keepdim=True).double() / 127).float()  # one rounding of the quotient: ties among the codes go by it
     codes = (x.double() / sx.double()).round().float()
     out = torch.matmul(codes, s["w"].float().t()) * sx * s["ws"]
     return {"out": (out if s["b"] is None else out + s["b"]).to(dt)}
@@ -383,6 +383,6 @@ def exact(case, seed):
                 dv[b, :n[b], h // G] += p.t() @ g
         return {"y": y} if c["kind"] == "xattn" else {"dq": dq, "dk": dk.contiguous(), "dv": dv.contiguous()}
     x = s["x"].double()
-    top = s["x"].float().abs().amax(1, keepdim=True) / 127
-    out = torch.round(x / top.double()) @ s["w"].double().t() * (top.double() * s["ws"].double())
+    top = (x.abs().amax(1, keepdim=True) / 127).float().double()  # the scale is held in 32 bits
+    out = torch.round(x / top) @ s["w"].double().t() * (top * s["ws"].double())
     return {"out": out if s["b"] is None else out + s["b"].double()}
