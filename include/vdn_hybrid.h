@@ -69,7 +69,8 @@ typedef enum {
 
 typedef enum {
   VDN_F32 = 0,  /* q, k, v, gates, text k/v in float32; exact mode (SIMT fp32 arithmetic) */
-  VDN_BF16 = 1  /* the same tensors in bfloat16; fp32 accumulation and fp32 state */
+  VDN_BF16 = 1, /* the same tensors in bfloat16; fp32 accumulation and fp32 state */
+  VDN_I8 = 2    /* signed 8-bit codes; only as the x_dtype of vdn_linear_int8 */
 } vdn_dtype;
 
 typedef struct {
@@ -256,7 +257,9 @@ enum {
   VDN_TAG_COMPOSE = 5,      /* chunk composition                                */
   VDN_TAG_SOFTMAX_BWD = 6,  /* softmax branch backward                          */
   VDN_TAG_LINEAR_BWD = 7,   /* linear branch backward                           */
-  VDN_TAG_PROJ = 8          /* output projection (vdn_proj_device_status)       */
+  VDN_TAG_PROJ = 8,         /* output projection (vdn_proj_device_status)       */
+  VDN_TAG_XATTN = 9,        /* cross-attention (vdn_cross_attn_device_status)   */
+  VDN_TAG_XATTN_BWD = 10    /* its backward                                     */
 };
 
 /* Reads the device status words left by the most recent call on this
@@ -509,6 +512,180 @@ vdn_status vdn_out_proj_fp8(const vdn_proj_cfg *cfg, const void *y, const void *
  * kernel gave up (the output is then incomplete); *where (if not NULL) gets
  * VDN_TAG_PROJ or VDN_TAG_NONE.  Errors: VDN_ERR_CUDA. */
 vdn_status vdn_proj_device_status(vdn_stream_t stream, unsigned *where);
+
+/* ------------------------------------- norm and rotation of queries and keys
+ * What a layer does to q and k before the core or the cross-attention: RMSNorm
+ * of every head and the rotation by position, in one pass over both.
+ *   z = x / sqrt(mean_i x_i^2 + eps) * w                 (over the d columns of a head)
+ *   (a, b) -> (a cos - b sin, a sin + b cos)             (pair j of the first rot columns)
+ * cos and sin of pair j stand in row p of the table, p the token's position on
+ * the pair's axis (one axis for text; frame, row and column for video). */
+enum {
+  VDN_PAIR_INTERLEAVED = 0, /* pair j is columns (2j, 2j + 1)       */
+  VDN_PAIR_SPLIT = 1        /* pair j is columns (j, j + rot / 2)   */
+};
+typedef struct {
+  int tokens;       /* rows of q and k                                                     >= 1 */
+  int Hq, Hk;       /* query and key heads; Hk = 0: no keys (k, k_out, wk are ignored)       */
+  int d;            /* head size: a multiple of 8, 8..256                                    */
+  int rot;          /* rotated leading columns: a multiple of 16, <= d; 0 = norm only         */
+  int pairing;      /* VDN_PAIR_*                                                            */
+  int axes;         /* position axes 1..3 (with rot = 0: still the width of pos)             */
+  int sections[3];  /* pairs of each axis, in order: axis 0 has the first sections[0] pairs;
+                       >= 0, the first `axes` of them sum to rot / 2                          */
+  int table_rows;   /* rows of the table (positions 0 .. table_rows - 1)  >= 1 unless rot = 0  */
+  int per_head;     /* 0: one weight row [d] for all heads; 1: a row for each head            */
+  int dtype;        /* vdn_dtype of q, k, q_out, k_out: VDN_F32 or VDN_BF16                   */
+  int grad_dtype;   /* backward: vdn_dtype of dq_out and dk_out; VDN_F32 when dtype is         */
+  float eps;        /* <= 0 selects 1e-6                                                     */
+  long long q_stride, k_stride; /* elements from one token of q (k) to the next, so that they can be
+                       slices of a packed projection; 0 = dense (H*d); else >= H*d and a
+                       multiple of 16 bytes                                                  */
+} vdn_qk_cfg;
+typedef struct {
+  const void *q, *k;      /* [tokens, H, d], head rows dense, tokens q_stride (k_stride) apart   */
+  const float *wq, *wk;   /* [d], or [H, d] with per_head; NULL = ones                        */
+  const float *table;     /* [table_rows, rot / 2, 2]: (cos, sin); NULL iff rot = 0            */
+  const int *pos;         /* [tokens, axes] int32 in device memory.  A token with a position
+                             outside [0, table_rows) on some axis is skipped: its rows of q_out and k_out stay
+                             as they were, and its gradients are zero.  NULL (axes = 1 only) =
+                             the token's own index; then table_rows >= tokens unless rot = 0.
+                             With rot = 0 and pos given, table_rows still bounds it.          */
+  void *q_out, *k_out;    /* [tokens, H, d] dense; no overlap with the inputs                 */
+} vdn_qk_args;
+
+/* Enqueue on `stream`; one kernel, no workspace.  fp32 arithmetic, one rounding
+ * to dtype at the end.  Errors: VDN_ERR_INVALID_ARG (sizes, enums, a NULL or
+ * misaligned pointer: 16 bytes for q, k, table, q_out, k_out, 4 for the
+ * others), VDN_ERR_UNSUPPORTED (more than 65535 heads), VDN_ERR_CUDA. */
+vdn_status vdn_qk_norm_rope(const vdn_qk_cfg *cfg, const vdn_qk_args *args, vdn_stream_t stream);
+
+typedef struct {
+  const void *dq_out, *dk_out; /* gradients of q_out and k_out, [tokens, H, d] dense, grad_dtype  */
+  void *dq, *dk;               /* [tokens, H, d] dense, dtype, overwritten                        */
+  float *dwq, *dwk;            /* like wq and wk, float32, overwritten; each may be NULL.  Also
+                                  when wq / wk are NULL (the gradient at ones)                   */
+  void *workspace;             /* >= vdn_qk_norm_rope_bwd_workspace_size(cfg), 256-byte aligned; may
+                                  be NULL when dwq and dwk are                                   */
+  size_t workspace_bytes;
+} vdn_qk_grads;
+
+/* Bytes of scratch for the weights' gradient; 0 if cfg is invalid. */
+size_t vdn_qk_norm_rope_bwd_workspace_size(const vdn_qk_cfg *cfg);
+
+/* The gradients of vdn_qk_norm_rope (args->q_out and k_out are not read).
+ * Nothing of the forward is kept: the norm is recomputed from q and k.  The
+ * weights' gradient is summed in a fixed order (the same bits on every run of
+ * the same device).  Errors as vdn_qk_norm_rope; VDN_ERR_WORKSPACE. */
+vdn_status vdn_qk_norm_rope_bwd(const vdn_qk_cfg *cfg, const vdn_qk_args *args, const vdn_qk_grads *grads,
+                                vdn_stream_t stream);
+
+/* ------------------------------------ cross-attention with lengths, and its backward
+ * Softmax cross-attention of Tq query tokens for each of B batch elements to an
+ * encoder's states of another length.  It generalises vdn_text_cross_attn: a
+ * number of valid states for each batch element, key heads shared by groups of
+ * query heads, float32 tensors, one query token up to long sequences, the
+ * log-sum-exp, and gradients.  For query head h and key head h / (H / Hkv):
+ *   o = softmax(s q K^T) V over the first kv_len[b] states of batch element b;
+ * with no valid state o = 0 and lse = -inf.  States past kv_len[b] are not used,
+ * whatever they hold. */
+typedef struct {
+  int B, Tq;        /* batch elements, query tokens of each                              >= 1 */
+  int L;            /* encoder states allocated for each batch element                   >= 1 */
+  int H, Hkv;       /* query heads; key heads, a divisor of H                                 */
+  int d;            /* head size: 32, 64 or 128                                              */
+  int dtype;        /* vdn_dtype of q, k, v, y and of their gradients                        */
+  float scale;      /* s; <= 0 selects 1 / sqrt(d)                                           */
+  long long k_stride, v_stride; /* elements from one state of k (v) to the next, so that they can be
+                       slices of a packed projection; 0 = dense (Hkv*d); else >= Hkv*d and a
+                       multiple of 16 bytes.  Batch elements are L times that apart.           */
+} vdn_xattn_cfg;
+typedef struct {
+  const void *q;       /* [B, Tq, H, d] dense                                                */
+  const void *k, *v;   /* [B, L, Hkv, d], head rows dense                                     */
+  const int *kv_len;   /* [B] int32 in device memory, clamped to [0, L]; NULL = L everywhere   */
+  void *y;             /* [B, Tq, H, d] dense: the forward's output; read by the backward      */
+  float *lse;          /* [B, Tq, H]: ln sum_j exp(s q k_j); forward: NULL = not written;
+                          backward: what the forward wrote                                   */
+  void *workspace;     /* scratch, 256-byte aligned; its first 256 bytes are status words       */
+  size_t workspace_bytes;
+} vdn_xattn_args;
+
+/* Bytes of workspace for the forward, and for the backward; 0 if cfg is invalid. */
+size_t vdn_cross_attn_workspace_size(const vdn_xattn_cfg *cfg);
+size_t vdn_cross_attn_bwd_workspace_size(const vdn_xattn_cfg *cfg);
+
+/* Which implementation runs (backward = 0 or 1): 0 = SIMT fp32, 1 = tcgen05
+ * tensor cores, 2 = the kernel for few query rows; -1 = not supported. */
+int vdn_cross_attn_impl(const vdn_xattn_cfg *cfg, int backward);
+
+/* Enqueue the forward on `stream`.  Errors: VDN_ERR_INVALID_ARG (sizes, Hkv not
+ * a divisor of H, a NULL or misaligned pointer: 16 bytes for q, k, v, y, 4 for
+ * kv_len and lse), VDN_ERR_UNSUPPORTED (another head size, tensors past the
+ * index limits: B*Tq, B*L and the launch's blocks below 2^31),
+ * VDN_ERR_WORKSPACE, VDN_ERR_CUDA. */
+vdn_status vdn_cross_attn(const vdn_xattn_cfg *cfg, const vdn_xattn_args *args, vdn_stream_t stream);
+
+typedef struct {
+  const void *dy;        /* gradient of y, [B, Tq, H, d] dense, dtype                            */
+  void *dq;              /* [B, Tq, H, d] dense, dtype, overwritten                              */
+  void *dk, *dv;         /* [B, L, Hkv, d] dense, dtype, overwritten; zero past kv_len[b]         */
+} vdn_xattn_grads;
+
+/* Enqueue the backward on `stream`: the gradients of q, k and v (the softmax
+ * is recomputed from lse).  No atomics: the same bits on every run.  In bf16 the products take P
+ * and dS rounded to bf16, accumulated in fp32.  Errors as the forward; y, lse
+ * and the three gradients are required (16 bytes; lse 4). */
+vdn_status vdn_cross_attn_bwd(const vdn_xattn_cfg *cfg, const vdn_xattn_args *args, const vdn_xattn_grads *grads,
+                              vdn_stream_t stream);
+
+/* Status words of the last cross-attention call (either direction) on this
+ * workspace (synchronises `stream`): VDN_OK, or VDN_ERR_TIMEOUT when a bounded
+ * wait gave up, with VDN_TAG_XATTN or VDN_TAG_XATTN_BWD in *where. */
+vdn_status vdn_cross_attn_device_status(const void *workspace, vdn_stream_t stream, unsigned *where);
+
+/* ------------------------------------------------ 8-bit integer linear layers
+ * Beside the FP8 layers (one scale per tensor): signed 8-bit codes with a scale
+ * for every token of x and every output channel of the weight.
+ *   s[m] = amax_k |x[m, k]| / 127,  q[m, k] = round(x[m, k] / s[m]), half to even (exactly)
+ *   out[m, n] = (sum_k q[m, k] w[n, k]) * s[m] * w_scale[n] + bias[n]
+ * The sum is exact in 32-bit integers.  A row with amax below 2^-119 has s = 1
+ * and codes 0; a row that holds an infinity or a NaN has s = NaN, codes 0. */
+
+/* codes and scale of every row of x [rows, cols] (x_dtype VDN_F32 or VDN_BF16;
+ * a weight is quantised the same way, one output channel a row).  q int8
+ * [rows, cols], scale float32 [rows]; x and q 16-byte aligned, cols a multiple of 16.
+ * Errors: VDN_ERR_INVALID_ARG, VDN_ERR_CUDA. */
+vdn_status vdn_quantize_int8(const void *x, int x_dtype, int rows, int cols, void *q, float *scale, vdn_stream_t stream);
+
+typedef struct {
+  int M;          /* rows (tokens)                                                       >= 1 */
+  int K;          /* inputs; a multiple of 16, 16 .. 131056 (the int32 sum cannot overflow)    */
+  int N;          /* output channels; a multiple of 16                                  >= 16 */
+  int x_dtype;    /* VDN_F32, VDN_BF16: x is quantised in the call; VDN_I8: x holds codes      */
+  int out_dtype;  /* VDN_F32 or VDN_BF16 (rounded to nearest even)                            */
+} vdn_int8_cfg;
+typedef struct {
+  const void *x;          /* [M, K] row-major, x_dtype                                        */
+  const float *x_scale;   /* [M]; required with VDN_I8, else NULL                              */
+  const void *w;          /* int8 codes [N, K] row-major                                      */
+  const float *w_scale;   /* [N]                                                              */
+  const float *bias;      /* [N] or NULL                                                      */
+  void *out;              /* [M, N] row-major, out_dtype                                       */
+  void *workspace;        /* codes and scales of x, 256-byte aligned; NULL when the size is 0    */
+  size_t workspace_bytes; /* >= vdn_linear_int8_workspace_size(cfg)                             */
+} vdn_int8_args;
+
+/* Bytes of workspace (0 with VDN_I8, for few rows, and for an invalid cfg). */
+size_t vdn_linear_int8_workspace_size(const vdn_int8_cfg *cfg);
+
+/* The layer on `stream`.  Up to 8 rows: one kernel, bound by the read of the
+ * weight; else on the tensor cores (tcgen05 kind::i8), whose bounded waits
+ * record a timeout in the words that vdn_proj_device_status reads.  Device
+ * pointers, 16-byte aligned (x_scale 4), no overlap of out with an input.
+ * Errors: VDN_ERR_INVALID_ARG, VDN_ERR_UNSUPPORTED (more than 2^30 output
+ * tiles), VDN_ERR_WORKSPACE, VDN_ERR_CUDA. */
+vdn_status vdn_linear_int8(const vdn_int8_cfg *cfg, const vdn_int8_args *args, vdn_stream_t stream);
 
 #ifdef __cplusplus
 }

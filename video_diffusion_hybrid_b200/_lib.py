@@ -16,7 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libvdn_hybrid.so")
 
 VDN_OK, VDN_ERR_INVALID_ARG, VDN_ERR_UNSUPPORTED, VDN_ERR_WORKSPACE, VDN_ERR_CUDA, VDN_ERR_TIMEOUT = range(6)
-VDN_F32, VDN_BF16 = 0, 1
+VDN_F32, VDN_BF16, VDN_I8 = 0, 1, 2
+PAIR_INTERLEAVED, PAIR_SPLIT = 0, 1
 STAGE_TEXT, STAGE_SOLVE, STAGE_SCAN, STAGE_SOFTMAX, STAGE_READ = 1, 2, 4, 8, 16
 STAGE_ALL = 31
 STAGE_SOFTMAX_BWD = 32  # vdn_hybrid_stage_impl key of the softmax branch's backward
@@ -26,7 +27,11 @@ EXPORTED = ("vdn_hybrid_attn_workspace_size", "vdn_hybrid_workspace_layout", "vd
             "vdn_status_string", "vdn_hybrid_attn_fwd_noalloc", "vdn_hybrid_noalloc_device_status", "vdn_out_proj", "vdn_text_cross_attn",
             "vdn_quantize_fp8", "vdn_out_proj_fp8", "vdn_hybrid_lin_bwd_workspace_size", "vdn_hybrid_lin_bwd",
             "vdn_hybrid_sm_bwd_workspace_size", "vdn_hybrid_sm_bwd", "vdn_hybrid_bwd_workspace_size", "vdn_hybrid_bwd",
-            "vdn_debug_set_read_wait_limit", "vdn_proj_device_status")
+            "vdn_debug_set_read_wait_limit", "vdn_proj_device_status",
+            "vdn_qk_norm_rope", "vdn_qk_norm_rope_bwd", "vdn_qk_norm_rope_bwd_workspace_size",
+            "vdn_cross_attn", "vdn_cross_attn_bwd", "vdn_cross_attn_workspace_size",
+            "vdn_cross_attn_bwd_workspace_size", "vdn_cross_attn_impl", "vdn_cross_attn_device_status",
+            "vdn_quantize_int8", "vdn_linear_int8", "vdn_linear_int8_workspace_size")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -73,6 +78,54 @@ class VdnGrads(C.Structure):
 class ProjCfg(C.Structure):
     """Mirror of ``vdn_proj_cfg``."""
     _fields_ = [("M", C.c_int), ("K", C.c_int), ("N", C.c_int), ("out_dtype", C.c_int)]
+
+
+class QkCfg(C.Structure):
+    """Mirror of ``vdn_qk_cfg``."""
+    _fields_ = [("tokens", C.c_int), ("Hq", C.c_int), ("Hk", C.c_int), ("d", C.c_int), ("rot", C.c_int),
+                ("pairing", C.c_int), ("axes", C.c_int), ("sections", C.c_int * 3), ("table_rows", C.c_int),
+                ("per_head", C.c_int), ("dtype", C.c_int), ("grad_dtype", C.c_int), ("eps", C.c_float),
+                ("q_stride", C.c_longlong), ("k_stride", C.c_longlong)]
+
+
+class QkArgs(C.Structure):
+    """Mirror of ``vdn_qk_args``."""
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("wq", C.c_void_p), ("wk", C.c_void_p), ("table", C.c_void_p),
+                ("pos", C.c_void_p), ("q_out", C.c_void_p), ("k_out", C.c_void_p)]
+
+
+class QkGrads(C.Structure):
+    """Mirror of ``vdn_qk_grads``."""
+    _fields_ = [("dq_out", C.c_void_p), ("dk_out", C.c_void_p), ("dq", C.c_void_p), ("dk", C.c_void_p),
+                ("dwq", C.c_void_p), ("dwk", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+class XattnCfg(C.Structure):
+    """Mirror of ``vdn_xattn_cfg``."""
+    _fields_ = [("B", C.c_int), ("Tq", C.c_int), ("L", C.c_int), ("H", C.c_int), ("Hkv", C.c_int), ("d", C.c_int),
+                ("dtype", C.c_int), ("scale", C.c_float), ("k_stride", C.c_longlong), ("v_stride", C.c_longlong)]
+
+
+class XattnArgs(C.Structure):
+    """Mirror of ``vdn_xattn_args``."""
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("kv_len", C.c_void_p), ("y", C.c_void_p),
+                ("lse", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+class XattnGrads(C.Structure):
+    """Mirror of ``vdn_xattn_grads``."""
+    _fields_ = [("dy", C.c_void_p), ("dq", C.c_void_p), ("dk", C.c_void_p), ("dv", C.c_void_p)]
+
+
+class Int8Cfg(C.Structure):
+    """Mirror of ``vdn_int8_cfg``."""
+    _fields_ = [("M", C.c_int), ("K", C.c_int), ("N", C.c_int), ("x_dtype", C.c_int), ("out_dtype", C.c_int)]
+
+
+class Int8Args(C.Structure):
+    """Mirror of ``vdn_int8_args``."""
+    _fields_ = [("x", C.c_void_p), ("x_scale", C.c_void_p), ("w", C.c_void_p), ("w_scale", C.c_void_p),
+                ("bias", C.c_void_p), ("out", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
 
 
 class VdnLayout(C.Structure):
@@ -168,6 +221,24 @@ def lib() -> C.CDLL:
         L.vdn_proj_device_status.argtypes = [C.c_void_p, C.POINTER(C.c_uint)]
         L.vdn_debug_set_read_wait_limit.restype = C.c_int
         L.vdn_debug_set_read_wait_limit.argtypes = [C.c_ulonglong]
+        for name, types in (("vdn_qk_norm_rope", (QkCfg, QkArgs)), ("vdn_qk_norm_rope_bwd", (QkCfg, QkArgs, QkGrads)),
+                            ("vdn_cross_attn", (XattnCfg, XattnArgs)),
+                            ("vdn_cross_attn_bwd", (XattnCfg, XattnArgs, XattnGrads)),
+                            ("vdn_linear_int8", (Int8Cfg, Int8Args))):
+            fn = getattr(L, name)
+            fn.restype = C.c_int
+            fn.argtypes = [C.POINTER(t) for t in types] + [C.c_void_p]
+        for name, cfg in (("vdn_qk_norm_rope_bwd_workspace_size", QkCfg), ("vdn_cross_attn_workspace_size", XattnCfg),
+                          ("vdn_cross_attn_bwd_workspace_size", XattnCfg), ("vdn_linear_int8_workspace_size", Int8Cfg)):
+            fn = getattr(L, name)
+            fn.restype = C.c_size_t
+            fn.argtypes = [C.POINTER(cfg)]
+        L.vdn_cross_attn_impl.restype = C.c_int
+        L.vdn_cross_attn_impl.argtypes = [C.POINTER(XattnCfg), C.c_int]
+        L.vdn_cross_attn_device_status.restype = C.c_int
+        L.vdn_cross_attn_device_status.argtypes = [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint)]
+        L.vdn_quantize_int8.restype = C.c_int
+        L.vdn_quantize_int8.argtypes = [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]
         L.vdn_status_string.restype = C.c_char_p
         L.vdn_status_string.argtypes = [C.c_int]
         _lib = L
@@ -389,3 +460,69 @@ def vdn_proj_device_status(stream=None) -> tuple:
     where = C.c_uint(0)
     st = lib().vdn_proj_device_status(_stream_handle(stream), C.byref(where))
     return st, where.value
+
+
+# ------------------------------------------ the layer's operators around the core
+def _checked(st: int, where: str, check: bool) -> int:
+    if check and st != VDN_OK:
+        raise VdnError(st, where)
+    return st
+
+
+def vdn_qk_norm_rope(cfg: QkCfg, args: QkArgs, stream=None, check: bool = True) -> int:
+    """RMSNorm of the query and key heads and their rotation, one pass."""
+    return _checked(lib().vdn_qk_norm_rope(cfg, args, _stream_handle(stream)), "vdn_qk_norm_rope", check)
+
+
+def vdn_qk_norm_rope_bwd_workspace_size(cfg: QkCfg) -> int:
+    return int(lib().vdn_qk_norm_rope_bwd_workspace_size(cfg))
+
+
+def vdn_qk_norm_rope_bwd(cfg: QkCfg, args: QkArgs, grads: QkGrads, stream=None, check: bool = True) -> int:
+    """The gradients of vdn_qk_norm_rope."""
+    return _checked(lib().vdn_qk_norm_rope_bwd(cfg, args, grads, _stream_handle(stream)), "vdn_qk_norm_rope_bwd", check)
+
+
+def vdn_cross_attn_workspace_size(cfg: XattnCfg) -> int:
+    return int(lib().vdn_cross_attn_workspace_size(cfg))
+
+
+def vdn_cross_attn_bwd_workspace_size(cfg: XattnCfg) -> int:
+    return int(lib().vdn_cross_attn_bwd_workspace_size(cfg))
+
+
+def vdn_cross_attn_impl(cfg: XattnCfg, backward: bool = False) -> int:
+    return int(lib().vdn_cross_attn_impl(cfg, int(backward)))
+
+
+def vdn_cross_attn(cfg: XattnCfg, args: XattnArgs, stream=None, check: bool = True) -> int:
+    """Cross-attention to an encoder's states, a length for each batch element."""
+    return _checked(lib().vdn_cross_attn(cfg, args, _stream_handle(stream)), "vdn_cross_attn", check)
+
+
+def vdn_cross_attn_bwd(cfg: XattnCfg, args: XattnArgs, grads: XattnGrads, stream=None, check: bool = True) -> int:
+    """The gradients of vdn_cross_attn (args.y and args.lse hold the forward's)."""
+    return _checked(lib().vdn_cross_attn_bwd(cfg, args, grads, _stream_handle(stream)), "vdn_cross_attn_bwd", check)
+
+
+def vdn_cross_attn_device_status(workspace, stream=None) -> tuple:
+    """(status, kernel tag) of the last cross-attention call on this workspace
+    (synchronises the stream)."""
+    where = C.c_uint(0)
+    st = lib().vdn_cross_attn_device_status(_ptr(workspace), _stream_handle(stream), C.byref(where))
+    return st, int(where.value)
+
+
+def vdn_quantize_int8(x, x_dtype: int, rows: int, cols: int, q, scale, stream=None, check: bool = True) -> int:
+    """Signed 8-bit codes of every row of x and the row's scale amax / 127."""
+    return _checked(lib().vdn_quantize_int8(_ptr(x), x_dtype, rows, cols, _ptr(q), _ptr(scale), _stream_handle(stream)),
+                    "vdn_quantize_int8", check)
+
+
+def vdn_linear_int8_workspace_size(cfg: Int8Cfg) -> int:
+    return int(lib().vdn_linear_int8_workspace_size(cfg))
+
+
+def vdn_linear_int8(cfg: Int8Cfg, args: Int8Args, stream=None, check: bool = True) -> int:
+    """out = (x w^T) with 8-bit codes, a scale per token and per channel, and a bias."""
+    return _checked(lib().vdn_linear_int8(cfg, args, _stream_handle(stream)), "vdn_linear_int8", check)

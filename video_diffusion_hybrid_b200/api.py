@@ -201,3 +201,266 @@ class HybridAttention:
         cc = cc.view(2, c.B, C, c.H, d, d)
         lam = self.workspace[lay["chunk_lam"]:lay["chunk_lam"] + 4 * n].view(torch.float32).view(c.B, C, c.H)
         return {"P": p16[:, :, :, 0] + p16[:, :, :, 1], "Cf": cc[0], "Cb": cc[1], "Lam": lam}
+
+
+# ------------------------------------------ the layer's operators around the core
+def _dtype_of(t: torch.Tensor) -> int:
+    if t.dtype == torch.bfloat16:
+        return L.VDN_BF16
+    if t.dtype == torch.float32:
+        return L.VDN_F32
+    raise TypeError(f"bfloat16 or float32 expected, got {t.dtype}")
+
+
+def _need(t, name: str, shape, dtype, device) -> None:
+    """A dense tensor of this shape, type and device (None passes)."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _head_rows(t: torch.Tensor, name: str, lead: tuple, H: int, d: int, dtype, device) -> int:
+    """Checks a [*lead, H, d] tensor whose head rows are dense and whose tokens
+    lie one stride apart (a slice of a packed projection); returns that stride
+    in elements."""
+    if tuple(t.shape) != (*lead, H, d) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {(*lead, H, d)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    # the stride of an axis of size one says nothing
+    if (d > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != d):
+        raise ValueError(f"{name}: the head rows have to be dense, got strides {t.stride()}")
+    stride, span = None, 0
+    for size, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if st < H * d or (stride is not None and st != span):
+            raise ValueError(f"{name}: the tokens have to lie one stride apart, got strides {t.stride()}")
+        stride = st if stride is None else stride
+        span = st * size
+    return H * d if stride is None else stride
+
+
+class _Streamed:
+    """What the layer's operators share: a device of their own, and calls that
+    run with that device current."""
+
+    def __init__(self, device):
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def _call(self, fn, *args, stream=None):
+        if torch.cuda.current_device() == self.device.index:
+            return fn(*args, stream)
+        with torch.cuda.device(self.device):
+            return fn(*args, stream)
+
+    def _new(self, shape, dtype, stream=None) -> torch.Tensor:
+        """A tensor that belongs to the stream of the call: its memory is not
+        handed out again before that stream's work is done.  Scratch is new on
+        every call, so calls on several streams and captured graphs do not share it."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+class QKNormRope(_Streamed):
+    """RMSNorm of every query and key head and the rotation by position, in one
+    pass (``vdn_qk_norm_rope``), and its gradients.  q [..., Hq, d] and
+    k [..., Hk, d] may be slices of a packed projection; the outputs are dense
+    and new on every call.
+
+    wq, wk: float32 [d] (or [H, d] with per_head), None = ones.  table: float32
+    [rows, rot / 2, 2] (cos, sin), see ``rope_table``.  pos: int32 [..., axes]
+    (or [...] for one axis); None = the token's index.  A token with a position
+    outside the table is skipped: its output rows are left as they were."""
+
+    def __init__(self, Hq: int, Hk: int, d: int, *, rot: int | None = None, pairing: str = "interleaved", sections=None,
+                 per_head: bool = False, eps: float = 1e-6, device="cuda"):
+        super().__init__(device)
+        self.Hq, self.Hk, self.d, self.per_head = Hq, Hk, d, per_head
+        self.rot = d if rot is None else rot
+        self.sections = tuple(sections) if sections is not None else (self.rot // 2,)
+        pair = {"interleaved": L.PAIR_INTERLEAVED, "split": L.PAIR_SPLIT}
+        if pairing not in pair or not 1 <= len(self.sections) <= 3:
+            raise L.VdnError(L.VDN_ERR_INVALID_ARG, "QKNormRope")
+        self.axes = len(self.sections)
+        self.base = dict(Hq=Hq, Hk=Hk, d=d, rot=self.rot, pairing=pair[pairing], axes=self.axes,
+                         per_head=int(per_head), eps=eps)
+
+    def _cfg_args(self, q, k, wq, wk, table, pos):
+        lead, dt = tuple(q.shape[:-2]), q.dtype
+        qs = _head_rows(q, "q", lead, self.Hq, self.d, dt, self.device)
+        ks = _head_rows(k, "k", lead, self.Hk, self.d, dt, self.device) if self.Hk else 0
+        n = 1
+        for s in lead:
+            n *= s
+        f32 = torch.float32
+        _need(wq, "wq", (self.Hq, self.d) if self.per_head else (self.d,), f32, self.device)
+        _need(wk, "wk", (self.Hk, self.d) if self.per_head else (self.d,), f32, self.device)
+        rows = 0
+        if self.rot:
+            rows = table.shape[0]
+            _need(table, "table", (rows, self.rot // 2, 2), f32, self.device)
+        if pos is not None:
+            _need(pos, "pos", lead if self.axes == 1 and pos.dim() == len(lead) else (*lead, self.axes), torch.int32, self.device)
+            rows = rows or 2**31 - 1
+        cfg = L.QkCfg(tokens=n, table_rows=rows, dtype=_dtype_of(q), q_stride=qs, k_stride=ks, **self.base)
+        for i, s in enumerate(self.sections):
+            cfg.sections[i] = s
+        args = L.QkArgs(q=q.data_ptr(), k=k.data_ptr() if self.Hk else None, wq=L._ptr(wq), wk=L._ptr(wk),
+                        table=table.data_ptr() if self.rot else None, pos=L._ptr(pos))
+        return cfg, args
+
+    def __call__(self, q, k, wq=None, wk=None, table=None, pos=None, out=None, stream=None):
+        """(q_out, k_out), dense, of q's type; `out`: a pair of tensors to write."""
+        cfg, args = self._cfg_args(q, k, wq, wk, table, pos)
+        if out is None:
+            out = (self._new(q.shape, q.dtype, stream), self._new(k.shape, q.dtype, stream) if self.Hk else None)
+        else:
+            _need(out[0], "q_out", q.shape, q.dtype, self.device)
+            _need(out[1], "k_out", k.shape if self.Hk else (), q.dtype, self.device)
+        args.q_out, args.k_out = out[0].data_ptr(), L._ptr(out[1])
+        self._call(L.vdn_qk_norm_rope, cfg, args, stream=stream)
+        return out
+
+    def backward(self, q, k, wq, wk, table, dq_out, dk_out, pos=None, stream=None) -> dict:
+        """dq, dk (q's type) and dwq, dwk (float32) from the gradients of the
+        outputs (float32, or q's type)."""
+        cfg, args = self._cfg_args(q, k, wq, wk, table, pos)
+        cfg.grad_dtype = _dtype_of(dq_out)
+        _need(dq_out, "dq_out", q.shape, dq_out.dtype, self.device)
+        if self.Hk:
+            _need(dk_out, "dk_out", k.shape, dq_out.dtype, self.device)
+        ws = self._new(L.vdn_qk_norm_rope_bwd_workspace_size(cfg), torch.uint8, stream)
+        new = lambda shape, dt: self._new(shape, dt, stream)  # noqa: E731
+        wshape = (lambda h: (h, self.d)) if self.per_head else (lambda h: (self.d,))
+        g = {"dq": new(q.shape, q.dtype), "dwq": new(wshape(self.Hq), torch.float32)}
+        if self.Hk:
+            g["dk"], g["dwk"] = new(k.shape, q.dtype), new(wshape(self.Hk), torch.float32)
+        gr = L.QkGrads(L._ptr(dq_out), L._ptr(dk_out) if self.Hk else None, L._ptr(g["dq"]), L._ptr(g.get("dk")),
+                       L._ptr(g["dwq"]), L._ptr(g.get("dwk")), ws.data_ptr(), ws.numel())
+        self._call(L.vdn_qk_norm_rope_bwd, cfg, args, gr, stream=stream)
+        return g
+
+
+def rope_table(rows: int, sections, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """(cos, sin) of position * base^(-j / pairs) for the pairs j of every axis
+    section, float32 [rows, sum(sections), 2]; the angles are formed in float64."""
+    freq = np.concatenate([base ** (-np.arange(n, dtype=np.float64) / max(n, 1)) for n in sections])
+    a = np.arange(rows, dtype=np.float64)[:, None] * freq
+    return torch.from_numpy(np.stack([np.cos(a), np.sin(a)], -1).astype(np.float32)).to(device)
+
+
+class CrossAttention(_Streamed):
+    """Softmax cross-attention of Tq query tokens to L encoder states for each of
+    B batch elements (``vdn_cross_attn``), and its gradients.  k and v
+    [B, L, Hkv, d] may be slices of a packed projection; kv_len: int32 [B] in
+    device memory, None = L everywhere.  Outputs and scratch are new on every
+    call; with keep_lse the object owns the log-sum-exp, which the next forward
+    call overwrites."""
+
+    def __init__(self, B: int, Tq: int, L_: int, H: int, Hkv: int, d: int, *, dtype: str = "bf16", scale: float = 0.0,
+                 keep_lse: bool = False, device="cuda"):
+        super().__init__(device)
+        self.shape, self.kv_shape = (B, Tq, H, d), (B, L_, Hkv, d)
+        self.torch_dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+        self.cfg = L.XattnCfg(B=B, Tq=Tq, L=L_, H=H, Hkv=Hkv, d=d, dtype=L.VDN_BF16 if dtype == "bf16" else L.VDN_F32, scale=scale)
+        self.need, self.bwd_need = L.vdn_cross_attn_workspace_size(self.cfg), L.vdn_cross_attn_bwd_workspace_size(self.cfg)
+        if self.need == 0:
+            raise L.VdnError(L.VDN_ERR_INVALID_ARG, "vdn_cross_attn_workspace_size")
+        self.workspace = self.bwd_workspace = None  # the last calls'
+        # the log-sum-exp of every query row, which the backward takes
+        self.lse = torch.empty((B, Tq, H), dtype=torch.float32, device=self.device) if keep_lse else None
+
+    def _inputs(self, q, k, v, kv_len):
+        B, _, Hkv, d = self.kv_shape
+        _need(q, "q", self.shape, self.torch_dtype, self.device)
+        _need(kv_len, "kv_len", (B,), torch.int32, self.device)
+        self.cfg.k_stride = _head_rows(k, "k", self.kv_shape[:2], Hkv, d, self.torch_dtype, self.device)
+        self.cfg.v_stride = _head_rows(v, "v", self.kv_shape[:2], Hkv, d, self.torch_dtype, self.device)
+        return L.XattnArgs(q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), kv_len=L._ptr(kv_len))
+
+    def __call__(self, q, k, v, kv_len=None, out=None, stream=None) -> torch.Tensor:
+        a = self._inputs(q, k, v, kv_len)
+        if out is None:
+            out = self._new(self.shape, self.torch_dtype, stream)
+        else:
+            _need(out, "out", self.shape, self.torch_dtype, self.device)
+        self.workspace = self._new(self.need, torch.uint8, stream)
+        a.y, a.lse = out.data_ptr(), L._ptr(self.lse)
+        a.workspace, a.workspace_bytes = self.workspace.data_ptr(), self.workspace.numel()
+        self._call(L.vdn_cross_attn, self.cfg, a, stream=stream)
+        return out
+
+    def backward(self, q, k, v, y, lse, dy, kv_len=None, stream=None) -> dict:
+        """dq, dk, dv from the forward's output y and log-sum-exp."""
+        a = self._inputs(q, k, v, kv_len)
+        _need(y, "y", self.shape, self.torch_dtype, self.device)
+        _need(dy, "dy", self.shape, self.torch_dtype, self.device)
+        _need(lse, "lse", self.shape[:3], torch.float32, self.device)
+        self.bwd_workspace = self._new(self.bwd_need, torch.uint8, stream)
+        a.y, a.lse = y.data_ptr(), lse.data_ptr()
+        a.workspace, a.workspace_bytes = self.bwd_workspace.data_ptr(), self.bwd_workspace.numel()
+        new = lambda shape: self._new(shape, self.torch_dtype, stream)  # noqa: E731
+        g = {"dq": new(self.shape), "dk": new(self.kv_shape), "dv": new(self.kv_shape)}
+        gr = L.XattnGrads(dy.data_ptr(), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr())
+        self._call(L.vdn_cross_attn_bwd, self.cfg, a, gr, stream=stream)
+        return g
+
+    def status(self, backward: bool = False, stream=None) -> tuple:
+        """(status, kernel tag) of the last forward (or backward) call's bounded waits."""
+        ws = self.bwd_workspace if backward else self.workspace
+        return self._call(L.vdn_cross_attn_device_status, ws, stream=stream)
+
+
+def quantize_int8(x: torch.Tensor, stream=None) -> tuple:
+    """Signed 8-bit codes of every row of x [rows, cols] and the rows' scales
+    (``vdn_quantize_int8``); a weight [out, in] gets a scale per output channel."""
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("quantize_int8: expected a contiguous matrix")
+    on = _Streamed(x.device)
+    q, scale = on._new(x.shape, torch.int8, stream), on._new(x.shape[:1], torch.float32, stream)
+    on._call(L.vdn_quantize_int8, x, _dtype_of(x), x.shape[0], x.shape[1], q, scale, stream=stream)
+    return q, scale
+
+
+class Int8Linear(_Streamed):
+    """A linear layer on signed 8-bit codes (``vdn_linear_int8``): w int8
+    [N, K] with w_scale float32 [N] (``quantize_int8`` of the weight), bias
+    float32 [N] or None.  The call quantises x [..., K] (bfloat16 or float32) by
+    rows, or takes codes (int8) with x_scale.  Outputs and scratch are new on
+    every call."""
+
+    def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, bias=None, *, out_dtype: str = "bf16"):
+        super().__init__(w.device)
+        self.N, self.K = w.shape
+        _need(w, "w", (self.N, self.K), torch.int8, self.device)
+        _need(w_scale, "w_scale", (self.N,), torch.float32, self.device)
+        _need(bias, "bias", (self.N,), torch.float32, self.device)
+        self.w, self.w_scale, self.bias = w, w_scale, bias
+        self.out_torch = {"bf16": torch.bfloat16, "f32": torch.float32}[out_dtype]
+        self.out_dtype = L.VDN_BF16 if out_dtype == "bf16" else L.VDN_F32
+
+    def __call__(self, x: torch.Tensor, x_scale=None, out=None, stream=None) -> torch.Tensor:
+        codes = x.dtype == torch.int8
+        if x.shape[-1] != self.K or not x.is_contiguous() or x.device != self.device:
+            raise ValueError(f"Int8Linear: expected a contiguous [..., {self.K}] tensor on {self.device}")
+        M = x.numel() // self.K
+        _need(x_scale, "x_scale", x.shape[:-1], torch.float32, self.device)
+        cfg = L.Int8Cfg(M=M, K=self.K, N=self.N, x_dtype=L.VDN_I8 if codes else _dtype_of(x), out_dtype=self.out_dtype)
+        need = L.vdn_linear_int8_workspace_size(cfg)
+        ws = self._new(need, torch.uint8, stream) if need else None
+        shape = (*x.shape[:-1], self.N)
+        if out is None:
+            out = self._new(shape, self.out_torch, stream)
+        else:
+            _need(out, "out", shape, self.out_torch, self.device)
+        a = L.Int8Args(x.data_ptr(), L._ptr(x_scale), self.w.data_ptr(), self.w_scale.data_ptr(), L._ptr(self.bias),
+                       out.data_ptr(), L._ptr(ws), need)
+        self._call(L.vdn_linear_int8, cfg, a, stream=stream)
+        return out

@@ -9,6 +9,9 @@
 // deepmagic post ("生成比播放還快", section 實測數據: the per-block latency
 // reaches its lowest figure with FP8 linear layers): e4m3 operands, the weight
 // given transposed ([n, K]), out = (s_y s_w) * sum_k q_y[m, k] q_w[n, k].
+// And the 8-bit integer linear layer: signed codes with a scale for each row of
+// A and each output channel, int32 accumulation (exact: |sum| <= 2^14 K < 2^31),
+// out = float(sum) s_a[m] s_w[n] + bias[n].
 //
 // Persistent kernel on CTA pairs (clusters of two CTAs on neighbouring SMs):
 // each pair computes 256 x 256 output tiles with tcgen05.mma.cta_group::2,
@@ -74,12 +77,33 @@ __device__ __forceinline__ void mma2_e4m3(uint32_t tmem_d, uint64_t adesc, uint6
       : "memory");
 }
 
+// signed 8-bit A and B, int32 D, both K-major (kind::i8: D format 2 = S32, A
+// and B formats 1 = signed)
+__host__ __device__ constexpr uint32_t idesc_s8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma2_s8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Operand kinds: bf16; e4m3 with one scale per tensor; signed 8-bit codes with
+// a scale per row and per channel.
+enum Kind { K_BF16, K_FP8, K_S8 };
+
 struct GemmArgs {
   int M, N, K;
   int tiles_n, tiles;  // column tiles, all tiles
   int nkb;             // K blocks of KBYTES per row
   void* out;
-  const float* scales;  // FP8: {s_y, s_w}; null for bf16
+  const float* scales;  // FP8: {s_y, s_w}
+  const float *row_scale, *col_scale, *bias;  // S8: [M], [N], [N] or null
 };
 
 // 32 accumulator values of one row to out (16-byte stores; `cols` valid)
@@ -96,9 +120,9 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&v)[3
                                                       pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
 }
 
-// FP8 = false: A bf16 [M, K] (K-major), B = W bf16 [K, N] (N contiguous: MN-major).
-// FP8 = true:  A e4m3 [M, K], B = W^T e4m3 [N, K] (both K-major).
-template <bool FP8, typename To>
+// K_BF16: A bf16 [M, K] (K-major), B = W bf16 [K, N] (N contiguous: MN-major).
+// K_FP8, K_S8: A [M, K], B = W^T [N, K], one byte each (both K-major).
+template <Kind KIND, typename To>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
 k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb) {
   enum { B_FULL = 0, B_EMPTY = ST, B_AFULL = 2 * ST, B_AEMPTY = 2 * ST + 2, B_DRAIN = 2 * ST + 4, NBARS };
@@ -108,6 +132,7 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  constexpr bool BYTE = KIND != K_BF16;
   // no early exit: both CTAs of the pair must reach the cluster barriers
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
@@ -151,7 +176,7 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
           if (it >= ST && !mbar_wait_cl(bar(B_EMPTY + s), (it / ST - 1) & 1, ctl)) { ok = false; break; }
           if (lead) mbar_expect_tx(bar(B_FULL + s), 2 * STAGE);
           const uint32_t sa = smem_u32(sm + s * STAGE), sb = sa + ABYTES;
-          if (FP8) {
+          if (BYTE) {
             tma_load_2d_pair(sa, &tma, lbar(B_FULL + s), kb * KBYTES, m0);
             tma_load_2d_pair(sb, &tmb, lbar(B_FULL + s), kb * KBYTES, n0);
           } else {
@@ -170,10 +195,11 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && lead) {
-      const uint32_t ID = FP8 ? idesc_e4m3(2 * TM, TN) : idesc_bf16(2 * TM, TN, true);
+      const uint32_t ID = KIND == K_FP8 ? idesc_e4m3(2 * TM, TN)
+                          : KIND == K_S8 ? idesc_s8(2 * TM, TN) : idesc_bf16(2 * TM, TN, true);
       const uint64_t a0 = sdesc(smem_u32(sm), 16, 1024);
-      // B: K-major (FP8), or MN-major with the two 64-column chunks 8 KB apart
-      const uint64_t b0 = FP8 ? sdesc(smem_u32(sm + ABYTES), 16, 1024) : sdesc(smem_u32(sm + ABYTES), 64 * 128, 1024);
+      // B: K-major (8-bit kinds), or MN-major with the two 64-column chunks 8 KB apart
+      const uint64_t b0 = BYTE ? sdesc(smem_u32(sm + ABYTES), 16, 1024) : sdesc(smem_u32(sm + ABYTES), 64 * 128, 1024);
       int it = 0, tc = 0;
       bool ok = true;
       for (int tile = pair; ok && tile < g.tiles; tile += npairs, ++tc) {
@@ -190,9 +216,11 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
           for (int k = 0; k < 4; ++k) {
             // A: 32 bytes of K per step inside the 128-byte swizzle row; B:
             // the same (K-major) or 16 rows of 128 bytes (MN-major)
-            const uint64_t ak = dadd(as, k * 32), bk = dadd(bs, FP8 ? k * 32 : k * 16 * 128);
-            if (FP8)
+            const uint64_t ak = dadd(as, k * 32), bk = dadd(bs, BYTE ? k * 32 : k * 16 * 128);
+            if (KIND == K_FP8)
               mma2_e4m3(d, ak, bk, ID, (kb | k) ? 1u : 0u);
+            else if (KIND == K_S8)
+              mma2_s8(d, ak, bk, ID, (kb | k) ? 1u : 0u);
             else
               mma2_bf16(d, ak, bk, ID, (kb | k) ? 1u : 0u);
           }
@@ -211,7 +239,7 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
     const int quad = warp & 3;
     const int trow = quad * 32 + lane;  // TMEM lane = row of this CTA's half
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
-    const float sc = FP8 ? __ldg(g.scales) * __ldg(g.scales + 1) : 1.0f;
+    const float sc = KIND == K_FP8 ? __ldg(g.scales) * __ldg(g.scales + 1) : 1.0f;
     To* out = static_cast<To*>(g.out);
     int tc = 0;
     for (int tile = pair; tile < g.tiles; tile += npairs, ++tc) {
@@ -221,16 +249,31 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
       const long long row = (long long)(tile / g.tiles_n) * 2 * TM + (long long)rank * TM + trow;
       const int n0 = (tile % g.tiles_n) * TN;
       const bool valid = row < g.M;
+      const float rs = KIND == K_S8 && valid ? __ldg(g.row_scale + row) : 0.f;
 #pragma unroll 1
       for (int c = 0; c < TN / 32; ++c) {
         float v[32];
         tmem_ld32(lane_addr + a * TN + 32 * c, v);
         tmem_wait_ld();
-        if (FP8) {
+        if (KIND == K_FP8) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= sc;
         }
         const int cols = g.N - (n0 + 32 * c);
+        if (KIND == K_S8) {
+          // columns in fours: N is a multiple of 16
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            if (i >= cols) continue;
+            const float4 w = __ldg(reinterpret_cast<const float4*>(g.col_scale + n0 + 32 * c + i));
+            const float4 b = g.bias ? __ldg(reinterpret_cast<const float4*>(g.bias + n0 + 32 * c + i))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = fmaf((float)__float_as_int(v[i]) * rs, w.x, b.x);
+            v[i + 1] = fmaf((float)__float_as_int(v[i + 1]) * rs, w.y, b.y);
+            v[i + 2] = fmaf((float)__float_as_int(v[i + 2]) * rs, w.z, b.z);
+            v[i + 3] = fmaf((float)__float_as_int(v[i + 3]) * rs, w.w, b.w);
+          }
+        }
         if (valid && cols > 0) store_row(out + row * g.N + n0 + 32 * c, v, cols);
       }
       tc_fence_before();
@@ -246,24 +289,23 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
 
 constexpr size_t gemm_smem() { return 1024 + (size_t)ST * STAGE + 32 * 8 + 16; }
 
-template <bool FP8, typename To>
-vdn_status launch(int M, int K, int N, const void* y, const void* w, const float* scales, void* out, cudaStream_t s) {
+template <Kind KIND, typename To>
+vdn_status launch(int M, int K, int N, const void* y, const void* w, void* out, cudaStream_t s, GemmArgs g) {
+  constexpr bool BYTE = KIND != K_BF16;
   CUtensorMap ma, mb;
-  if (FP8) {
+  if (BYTE) {
     if (!make_matrix_map_u8(&ma, y, M, K, TM) || !make_matrix_map_u8(&mb, w, N, K, TN / 2)) return VDN_ERR_CUDA;
   } else {
     if (!make_matrix_map(&ma, y, M, K, TM) || !make_matrix_map(&mb, w, K, N, 64)) return VDN_ERR_CUDA;
   }
-  GemmArgs g;
   g.M = M; g.N = N; g.K = K;
   g.tiles_n = (N + TN - 1) / TN;
   const long long tiles = (long long)((M + 2 * TM - 1) / (2 * TM)) * g.tiles_n;
   if (tiles > 0x3FFFFFFFLL) return VDN_ERR_UNSUPPORTED;
   g.tiles = (int)tiles;
-  g.nkb = (int)(((long long)K * (FP8 ? 1 : 2) + KBYTES - 1) / KBYTES);
+  g.nkb = (int)(((long long)K * (BYTE ? 1 : 2) + KBYTES - 1) / KBYTES);
   g.out = out;
-  g.scales = scales;
-  auto kern = k_gemm_tc<FP8, To>;
+  auto kern = k_gemm_tc<KIND, To>;
   const size_t smem = gemm_smem();
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return VDN_ERR_CUDA;
@@ -287,18 +329,34 @@ vdn_status launch(int M, int K, int N, const void* y, const void* w, const float
   return cudaGetLastError() == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
 
+bool clear_status(cudaStream_t s) {
+  uint32_t* st = status_of_proj();
+  return encode_fn() && st && cudaMemsetAsync(st, 0, sizeof(uint32_t) * 2, s) == cudaSuccess;
+}
+
 }  // namespace
 
 vdn_status out_proj(int M, int K, int N, int out_dtype, const void* y, const void* w, void* out, cudaStream_t s,
                     const float* scales) {
-  if (!encode_fn()) return VDN_ERR_CUDA;
-  uint32_t* st = status_of_proj();
-  if (!st || cudaMemsetAsync(st, 0, sizeof(uint32_t) * 2, s) != cudaSuccess) return VDN_ERR_CUDA;
+  if (!clear_status(s)) return VDN_ERR_CUDA;
+  GemmArgs g{};
+  g.scales = scales;
   if (scales)
-    return out_dtype == VDN_BF16 ? launch<true, __nv_bfloat16>(M, K, N, y, w, scales, out, s)
-                                 : launch<true, float>(M, K, N, y, w, scales, out, s);
-  return out_dtype == VDN_BF16 ? launch<false, __nv_bfloat16>(M, K, N, y, w, nullptr, out, s)
-                               : launch<false, float>(M, K, N, y, w, nullptr, out, s);
+    return out_dtype == VDN_BF16 ? launch<K_FP8, __nv_bfloat16>(M, K, N, y, w, out, s, g)
+                                 : launch<K_FP8, float>(M, K, N, y, w, out, s, g);
+  return out_dtype == VDN_BF16 ? launch<K_BF16, __nv_bfloat16>(M, K, N, y, w, out, s, g)
+                               : launch<K_BF16, float>(M, K, N, y, w, out, s, g);
+}
+
+vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
+                   const float* w_scale, const float* bias, void* out, cudaStream_t s) {
+  if (!clear_status(s)) return VDN_ERR_CUDA;
+  GemmArgs g{};
+  g.row_scale = a_scale;
+  g.col_scale = w_scale;
+  g.bias = bias;
+  return out_dtype == VDN_BF16 ? launch<K_S8, __nv_bfloat16>(M, K, N, a, w, out, s, g)
+                               : launch<K_S8, float>(M, K, N, a, w, out, s, g);
 }
 
 uint32_t* status_of_proj() {

@@ -106,6 +106,14 @@ vdn_status out_proj(int M, int K, int N, int out_dtype, const void* y, const voi
                     const float* scales = nullptr);
 // device address of the projection's status words (library-owned), or null
 uint32_t* status_of_proj();
+// out = float(a w^T) a_scale[m] w_scale[n] + bias[n]: signed 8-bit codes a [M, K], w [N, K]
+vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
+                   const float* w_scale, const float* bias, void* out, cudaStream_t s);
+// codes and scale of every row of x (vdn_int8.cu)
+cudaError_t launch_quantize_int8(const void* x, int dtype, int rows, int cols, void* q, float* scale, cudaStream_t s);
+// the 8-bit linear layer for few rows, quantising x inside (x_scale == null) or taking codes
+bool int8_few_supported(int M, int K, int N);
+cudaError_t launch_int8_few(const vdn_int8_cfg& c, const vdn_int8_args& a, cudaStream_t s);
 vdn_status quantize_fp8(const void* x, int dtype, long long n, void* q, float* scale, cudaStream_t s);
 // The chunk-composed scan where it helps: the compositions (one CTA per
 // chunk, batch-head and direction) take about one wave of the SMs, and then
@@ -164,5 +172,10 @@ bool sm_bwd_tc_supported(const Dims& d);
 // bytes of its scratch; off[0..7] (if not null): status, q16, k16, v16, dO16, lse2, delta, amax
 size_t sm_bwd_tc_workspace(const Dims& d, size_t* off);
 cudaError_t launch_sm_bwd_tc(const Dims& d, const Inputs& in, const SmTcArgs& a, cudaStream_t s);
+
+// RMSNorm and rotation of the query and key heads (vdn_qk_rope.cu)
+size_t qk_bwd_workspace(const vdn_qk_cfg& c);
+cudaError_t launch_qk_fwd(const vdn_qk_cfg& c, const vdn_qk_args& in, cudaStream_t s);
+cudaError_t launch_qk_bwd(const vdn_qk_cfg& c, const vdn_qk_args& in, const vdn_qk_grads& g, cudaStream_t s);
 
 }  // namespace vdn
