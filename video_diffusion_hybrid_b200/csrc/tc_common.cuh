@@ -406,6 +406,11 @@ EncodeTiled encode_fn();
 // head x `rows` tokens, 128-byte swizzle.
 bool make_token_map(CUtensorMap* m, const void* base, long long tokens, int H, int D, int rows);
 
+// The same with tokens `stride` elements apart and a box of 64 dims x `heads`
+// heads x `rows` tokens (token-major, then head).
+bool make_token_map_strided(CUtensorMap* m, const void* base, long long tokens, int H, int D, long long stride, int heads,
+                            int rows);
+
 // 2-D map over a row-major [rows][cols] bf16 matrix; box = 64 cols x
 // `box_rows` rows, 128-byte swizzle.
 bool make_matrix_map(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows);

@@ -20,16 +20,21 @@ EncodeTiled encode_fn() {
   return fn;
 }
 
-bool make_token_map(CUtensorMap* m, const void* base, long long tokens, int H, int D, int rows) {
+bool make_token_map_strided(CUtensorMap* m, const void* base, long long tokens, int H, int D, long long stride, int heads,
+                            int rows) {
   EncodeTiled fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)rows};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_token_map(CUtensorMap* m, const void* base, long long tokens, int H, int D, int rows) {
+  return make_token_map_strided(m, base, tokens, H, D, (long long)H * D, 1, rows);
 }
 
 bool make_matrix_map(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows) {

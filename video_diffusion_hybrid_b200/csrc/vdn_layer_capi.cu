@@ -97,6 +97,8 @@ XArgs xargs(const vdn_xattn_args* a, const vdn_xattn_grads* g) {
   return x;
 }
 
+bool on_tensor_cores(const vdn_xattn_cfg* c) { return c->dtype == VDN_BF16 && xattn_tc_supported(xdims(c, nullptr)); }
+
 // --------------------------------------------------------------- 8-bit layer
 vdn_status check_int8(const vdn_int8_cfg* c) {
   if (!c) return VDN_ERR_INVALID_ARG;
@@ -144,7 +146,8 @@ vdn_status vdn_qk_norm_rope_bwd(const vdn_qk_cfg* cfg, const vdn_qk_args* args, 
 }
 
 size_t vdn_cross_attn_workspace_size(const vdn_xattn_cfg* cfg) {
-  return check_x(cfg) == VDN_OK ? kAlign : 0;
+  if (check_x(cfg) != VDN_OK) return 0;
+  return kAlign + (on_tensor_cores(cfg) ? up(xattn_tc_scratch(xdims(cfg, nullptr))) : 0);
 }
 
 size_t vdn_cross_attn_bwd_workspace_size(const vdn_xattn_cfg* cfg) {
@@ -154,8 +157,7 @@ size_t vdn_cross_attn_bwd_workspace_size(const vdn_xattn_cfg* cfg) {
 
 int vdn_cross_attn_impl(const vdn_xattn_cfg* cfg, int backward) {
   if (check_x(cfg) != VDN_OK) return -1;
-  (void)backward;
-  return 0;
+  return !backward && on_tensor_cores(cfg) ? 1 : 0;
 }
 
 vdn_status vdn_cross_attn(const vdn_xattn_cfg* cfg, const vdn_xattn_args* args, vdn_stream_t stream) {
@@ -166,6 +168,7 @@ vdn_status vdn_cross_attn(const vdn_xattn_cfg* cfg, const vdn_xattn_args* args, 
   const XDims d = xdims(cfg, args);
   const XArgs a = xargs(args, nullptr);
   if (cudaMemsetAsync(a.status, 0, kAlign, s) != cudaSuccess) return VDN_ERR_CUDA;
+  if (on_tensor_cores(cfg)) return launch_xattn_tc(d, a, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
   return launch_xattn_simt(d, a, cfg->dtype == VDN_BF16, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
 
