@@ -152,12 +152,14 @@ size_t vdn_cross_attn_workspace_size(const vdn_xattn_cfg* cfg) {
 
 size_t vdn_cross_attn_bwd_workspace_size(const vdn_xattn_cfg* cfg) {
   if (check_x(cfg) != VDN_OK) return 0;
-  return kAlign + up(xattn_simt_bwd_scratch(xdims(cfg, nullptr)));
+  const XDims d = xdims(cfg, nullptr);
+  return kAlign + up(on_tensor_cores(cfg) ? xattn_tc_bwd_scratch(d) : xattn_simt_bwd_scratch(d));
 }
 
 int vdn_cross_attn_impl(const vdn_xattn_cfg* cfg, int backward) {
   if (check_x(cfg) != VDN_OK) return -1;
-  return !backward && on_tensor_cores(cfg) ? 1 : 0;
+  (void)backward;  // both directions alike
+  return on_tensor_cores(cfg) ? 1 : 0;
 }
 
 vdn_status vdn_cross_attn(const vdn_xattn_cfg* cfg, const vdn_xattn_args* args, vdn_stream_t stream) {
@@ -183,6 +185,7 @@ vdn_status vdn_cross_attn_bwd(const vdn_xattn_cfg* cfg, const vdn_xattn_args* ar
   const XDims d = xdims(cfg, args);
   const XArgs a = xargs(args, g);
   if (cudaMemsetAsync(a.status, 0, kAlign, s) != cudaSuccess) return VDN_ERR_CUDA;
+  if (on_tensor_cores(cfg)) return launch_xattn_tc_bwd(d, a, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
   return launch_xattn_simt_bwd(d, a, cfg->dtype == VDN_BF16, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
 

@@ -39,5 +39,8 @@ cudaError_t launch_xattn_simt_bwd(const XDims& d, const XArgs& a, bool bf16, cud
 bool xattn_tc_supported(const XDims& d);
 size_t xattn_tc_scratch(const XDims& d);
 cudaError_t launch_xattn_tc(const XDims& d, const XArgs& a, cudaStream_t s);
+// its backward (vdn_xattn_bwd_tc.cu); scratch: <dO, o> per query row and partial sums
+size_t xattn_tc_bwd_scratch(const XDims& d);
+cudaError_t launch_xattn_tc_bwd(const XDims& d, const XArgs& a, cudaStream_t s);
 
 }  // namespace vdn
