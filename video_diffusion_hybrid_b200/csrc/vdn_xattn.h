@@ -29,6 +29,37 @@ __device__ __forceinline__ int kv_valid(const XDims& d, int b) {
   return n < 0 ? 0 : n > d.L ? d.L : n;
 }
 
+// The items of a persistent kernel's CTA: every gridDim.x-th of a mixed-radix
+// count (d0 fastest).  Stepping adds the stride's digits, without divisions.
+struct ItemGrid {
+  int items, r0, r1, r2;   // all items, radices of the first three digits
+  int s0, s1, s2, s3;      // digits of the grid's size
+};
+inline ItemGrid item_grid(int items, int r0, int r1, int r2, int grid) {
+  return {items, r0, r1, r2, grid % r0, grid / r0 % r1, grid / r0 / r1 % r2, grid / r0 / r1 / r2};
+}
+struct ItemPos {
+  int item, d0, d1, d2, d3;
+  __device__ __forceinline__ void start(const ItemGrid& g) {
+    item = blockIdx.x;
+    int r = item;
+    d0 = r % g.r0; r /= g.r0;
+    d1 = r % g.r1; r /= g.r1;
+    d2 = r % g.r2; d3 = r / g.r2;
+  }
+  __device__ __forceinline__ bool on(const ItemGrid& g) const { return item < g.items; }
+  __device__ __forceinline__ void next(const ItemGrid& g) {
+    item += gridDim.x;
+    d0 += g.s0;
+    d1 += g.s1;
+    d2 += g.s2;
+    d3 += g.s3;
+    if (d0 >= g.r0) { d0 -= g.r0; ++d1; }
+    if (d1 >= g.r1) { d1 -= g.r1; ++d2; }
+    if (d2 >= g.r2) { d2 -= g.r2; ++d3; }
+  }
+};
+
 // SIMT, float32 arithmetic: any type, d = 32, 64 or 128 (vdn_xattn.cu)
 cudaError_t launch_xattn_simt(const XDims& d, const XArgs& a, bool bf16, cudaStream_t s);
 // needs the scratch of xattn_simt_bwd_scratch: <dO, o> per query row

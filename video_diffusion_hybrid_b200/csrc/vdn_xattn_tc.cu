@@ -61,9 +61,9 @@ __host__ __device__ constexpr uint32_t col_s(int t) { return 256u + 128u * t; }
 
 struct XtDev {
   int B, Tq, L, H, G;
-  int P, TT, HG;       // heads and tokens of a tile (P TT <= 128 rows), head groups H / P
-  int pairs, ns, alt;  // tile pairs over the tokens, splits of the states, tiles alternate over key tiles
-  int items;
+  int P, TT;           // heads and tokens of a tile (P TT <= 128 rows)
+  int ns, alt;         // splits of the states, tiles alternate over key tiles
+  ItemGrid grid;       // splits, tile pairs over the tokens, head groups, batch elements
   float scale;
   const int* kv_len;
   __nv_bfloat16* y;
@@ -80,25 +80,28 @@ struct Item {
   int sp;
 };
 
+// the same for every lane (and known to be: the reduction's result is a uniform register)
 __device__ __forceinline__ int valid_states(const XtDev& x, int b) {
   if (x.kv_len == nullptr) return x.L;
-  const int n = __ldg(x.kv_len + b);
-  return n < 0 ? 0 : n > x.L ? x.L : n;
+  return __reduce_max_sync(0xffffffffu, max(0, min(__ldg(x.kv_len + b), x.L)));
 }
 
-__device__ __forceinline__ Item decode(const XtDev& x, int item) {
+// call with the whole warp
+__device__ __forceinline__ Item decode(const XtDev& x, const ItemPos& p) {
   Item t;
-  t.sp = item % x.ns;
-  int r = item / x.ns;
-  const int qp = r % x.pairs;
-  r /= x.pairs;
-  t.hg = r % x.HG;
-  t.b = r / x.HG;
-  const int first = qp * (x.alt ? 1 : 2) * x.TT;
+  t.sp = p.d0;
+  t.hg = p.d2;
+  t.b = p.d3;
+  const int first = p.d1 * (x.alt ? 1 : 2) * x.TT;
   t.q0 = t.b * x.Tq + first;
   t.left = x.Tq - first;
-  const int n = valid_states(x, t.b), all = (n + BN - 1) / BN, per = (all + x.ns - 1) / x.ns;
-  const int lo = min(t.sp * per, all), hi = min(lo + per, all);
+  const int n = valid_states(x, t.b), all = (n + BN - 1) / BN;
+  int lo = 0, hi = all;
+  if (x.ns > 1) {
+    const int per = (all + x.ns - 1) / x.ns;
+    lo = min(t.sp * per, all);
+    hi = min(lo + per, all);
+  }
   t.nt = hi - lo;
   t.k0 = t.b * x.L + lo * BN;
   t.nk = min(n, hi * BN) - lo * BN;
@@ -113,18 +116,19 @@ __device__ __forceinline__ bool takes(const XtDev& x, const Item& it, int t, int
 
 // A CTA's key tiles in order; `n` counts them over all items (its ring position).
 struct Walk {
-  int item, j, n;
+  ItemPos pos;
+  int j, n;
   bool on;
   Item it;
-  __device__ __forceinline__ void settle(const XtDev& x) {  // the first item from `item` on that has key tiles
-    for (; item < x.items; item += gridDim.x) {
-      it = decode(x, item);
+  __device__ __forceinline__ void settle(const XtDev& x) {  // the first item from here on that has key tiles
+    for (; pos.on(x.grid); pos.next(x.grid)) {
+      it = decode(x, pos);
       if (it.nt > 0) return;
     }
     on = false;
   }
   __device__ __forceinline__ void start(const XtDev& x) {
-    item = blockIdx.x;
+    pos.start(x.grid);
     j = n = 0;
     on = true;
     settle(x);
@@ -133,7 +137,7 @@ struct Walk {
     ++n;
     if (++j < it.nt) return;
     j = 0;
-    item += gridDim.x;
+    pos.next(x.grid);
     settle(x);
   }
   // to the next key tile that tile t takes (this one included)
@@ -197,27 +201,28 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
 
   if (warp == 0) {
     // ------------------------------------------------------------ K producer
-    if (lane == 0) {
-      Walk w;
-      int issued = 0;
-      for (w.start(x); w.on; w.next(x)) {
-        const int s = w.n % KST;
-        if (w.n >= KST && !mbar_wait(bar(B_KEMPTY + s), (w.n / KST - 1) & 1, ctl)) break;
+    Walk w;
+    int issued = 0;
+    for (w.start(x); w.on; w.next(x)) {
+      const int s = w.n % KST;
+      if (w.n >= KST && !mbar_wait_warp(bar(B_KEMPTY + s), (w.n / KST - 1) & 1, ctl)) break;
+      if (lane == 0) {
         mbar_expect_tx(bar(B_KFULL + s), KVBYTES);
         for (int c = 0; c < NB; ++c)
           tma_load_3d(smem_u32(sK + s * KVBYTES + c * BN * 128), &tmk, bar(B_KFULL + s), c * 64, w.it.hg * x.P / x.G,
                       w.it.k0 + w.j * BN);
-        issued = w.n + 1;
       }
-      for (int n = max(issued - KST, 0); n < issued; ++n) mbar_drain(bar(B_KFULL + n % KST), (n / KST) & 1);
+      issued = w.n + 1;
     }
+    if (lane == 0)
+      for (int n = max(issued - KST, 0); n < issued; ++n) mbar_drain(bar(B_KFULL + n % KST), (n / KST) & 1);
   } else if (warp == 2) {
     // ------------------------------------------------------------ V producer
     Walk w;
     int issued = 0;
     for (w.start(x); w.on; w.next(x)) {
       const int s = w.n % VST;
-      if (w.n >= VST && !__all_sync(0xffffffffu, mbar_wait(bar(B_VEMPTY + s), (w.n / VST - 1) & 1, ctl))) break;
+      if (w.n >= VST && !mbar_wait_warp(bar(B_VEMPTY + s), (w.n / VST - 1) & 1, ctl)) break;
       if (lane == 0) {
         mbar_expect_tx(bar(B_VFULL + s), KVBYTES);
         for (int c = 0; c < NB; ++c)
@@ -227,7 +232,7 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
       issued = w.n + 1;
       const int valid = w.it.nk - w.j * BN;
       if (valid < BN) {  // rows past the last state: zeros
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_VFULL + s), (w.n / VST) & 1, ctl))) break;
+        if (!mbar_wait_warp(bar(B_VFULL + s), (w.n / VST) & 1, ctl)) break;
         for (int c = 0; c < NB; ++c) {
           uint4* base = reinterpret_cast<uint4*>(sV + s * KVBYTES + c * BN * 128);
           for (int i = valid * 8 + lane; i < BN * 8; i += 32) base[i] = make_uint4(0, 0, 0, 0);
@@ -240,111 +245,113 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
       for (int n = max(issued - VST, 0); n < issued; ++n) mbar_drain(bar(B_VFULL + n % VST), (n / VST) & 1);
   } else if (warp == 3) {
     // ------------------------------------------------------------ Q producer
-    if (lane == 0) {
-      const uint32_t bytes = (uint32_t)(x.P * x.TT) * 128u * NB;
-      int cnt[2] = {0, 0};  // loads into each tile
-      bool ok = true;
-      for (int item = blockIdx.x; ok && item < x.items; item += gridDim.x) {
-        const Item it = decode(x, item);
-        for (int t = 0; ok && t < 2; ++t) {
-          if (it.nt == 0 || !has_rows(x, it, t) || (x.alt && it.nt <= t)) continue;
-          if (cnt[t] > 0 && !mbar_wait(bar(B_QEMPTY + t), (cnt[t] - 1) & 1, ctl)) { ok = false; break; }
+    const uint32_t bytes = (uint32_t)(x.P * x.TT) * 128u * NB;
+    int cnt[2] = {0, 0};  // loads into each tile
+    bool ok = true;
+    ItemPos pos;
+    for (pos.start(x.grid); ok && pos.on(x.grid); pos.next(x.grid)) {
+      const Item it = decode(x, pos);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || it.nt == 0 || !has_rows(x, it, t) || (x.alt && it.nt <= t)) continue;
+        if (cnt[t] > 0 && !mbar_wait_warp(bar(B_QEMPTY + t), (cnt[t] - 1) & 1, ctl)) { ok = false; continue; }
+        if (lane == 0) {
           mbar_expect_tx(bar(B_QFULL + t), bytes);
           for (int c = 0; c < NB; ++c)
             tma_load_3d(smem_u32(sQ + t * QTILE + c * BM * 128), &tmq, bar(B_QFULL + t), c * 64, it.hg * x.P,
                         it.q0 + (x.alt ? 0 : t * x.TT));
-          ++cnt[t];
         }
+        ++cnt[t];
       }
+    }
+    if (lane == 0)
       for (int t = 0; t < 2; ++t)
         if (cnt[t] > 0) mbar_drain(bar(B_QFULL + t), (cnt[t] - 1) & 1);
-    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t ID_S = idesc_bf16(BM, BN, false);
-      constexpr uint32_t ID_O = idesc_bf16(BM, D, true);
-      const uint64_t qd0 = sdesc(smem_u32(sQ), 16, 1024), kd0 = sdesc(smem_u32(sK), 16, 1024);
-      const uint64_t vd0 = sdesc(smem_u32(sV), BN * 128, 1024);
-      const int ahead = x.alt ? 2 : 1;
-      Walk nx[2];        // each tile's next scores
-      int nq[2] = {0, 0};  // items begun by each tile
-      int ns[2] = {0, 0}, np[2] = {0, 0};  // key tiles whose scores, and whose O += P V, were issued
-      uint32_t fixes = 0;  // a bit for each stage: parity of its next hand-over by the V producer's zeroing
-      // S_t = Q_t K^T of the tile's next key tile, and the walk moves on
-      auto scores = [&](int t) -> bool {
-        Walk& w = nx[t];
-        const bool first = w.j == (x.alt ? t : 0);
-        const int s = w.n % KST;
-        if (first) {
-          if (!mbar_wait(bar(B_QFULL + t), nq[t] & 1, ctl)) return false;
-          ++nq[t];
-        }
-        if (!mbar_wait(bar(B_KFULL + s), (w.n / KST) & 1, ctl)) return false;
-        tc_fence_after();
-        const uint64_t qd = dadd(qd0, t * QTILE), kd = dadd(kd0, s * KVBYTES);
-        const uint32_t dst = tmem + col_s(t);
-        mma_bf16(dst, qd, kd, ID_S, 0u);
+    // (the whole warp, converged; one elected lane issues)
+    constexpr uint32_t ID_S = idesc_bf16(BM, BN, false);
+    constexpr uint32_t ID_O = idesc_bf16(BM, D, true);
+    const uint32_t el = elect_one();
+    const uint64_t qd0 = sdesc(smem_u32(sQ), 16, 1024), kd0 = sdesc(smem_u32(sK), 16, 1024);
+    const uint64_t vd0 = sdesc(smem_u32(sV), BN * 128, 1024);
+    const int ahead = x.alt ? 2 : 1;
+    Walk nx[2];          // each tile's next scores
+    int nq[2] = {0, 0};  // items begun by each tile
+    int ns[2] = {0, 0}, np[2] = {0, 0};  // key tiles whose scores, and whose O += P V, were issued
+    uint32_t fixes = 0;  // a bit for each stage: parity of its next hand-over by the V producer's zeroing
+    // S_t = Q_t K^T of the tile's next key tile, and the walk moves on
+    auto scores = [&](int t) -> bool {
+      Walk& w = nx[t];
+      const int s = w.n % KST;
+      if (w.j == (x.alt ? t : 0)) {
+        if (!mbar_wait_warp(bar(B_QFULL + t), nq[t] & 1, ctl)) return false;
+        ++nq[t];
+      }
+      if (!mbar_wait_warp(bar(B_KFULL + s), (w.n / KST) & 1, ctl)) return false;
+      tc_fence_after();
+      const uint64_t qd = dadd(qd0, t * QTILE), kd = dadd(kd0, s * KVBYTES);
+      const uint32_t dst = tmem + col_s(t);
 #pragma unroll
-        for (int k = 1; k < D / 16; ++k)
-          mma_bf16(dst, dadd(qd, (k >> 2) * (BM * 128) + (k & 3) * 32), dadd(kd, (k >> 2) * (BN * 128) + (k & 3) * 32), ID_S, 1u);
-        mma_commit(bar(B_SFULL + t));
-        ++ns[t];
-        if (x.alt || t == 1 || !has_rows(x, w.it, 1)) mma_commit(bar(B_KEMPTY + s));  // read by every tile that takes it
-        if (w.j + ahead >= w.it.nt) mma_commit(bar(B_QEMPTY + t));                    // the item's last scores of this tile
-        w.next(x);
-        w.seek(x, t);
-        return true;
-      };
+      for (int k = 0; k < D / 16; ++k)
+        mma_bf16_w(dst, dadd(qd, (k >> 2) * (BM * 128) + (k & 3) * 32), dadd(kd, (k >> 2) * (BN * 128) + (k & 3) * 32), ID_S,
+                   k > 0 ? 1u : 0u, el);
+      mma_commit_w(bar(B_SFULL + t), el);
+      ++ns[t];
+      if (x.alt || t == 1 || !has_rows(x, w.it, 1)) mma_commit_w(bar(B_KEMPTY + s), el);  // read by every tile that takes it
+      if (w.j + ahead >= w.it.nt) mma_commit_w(bar(B_QEMPTY + t), el);                    // the item's last scores of this tile
+      w.next(x);
+      w.seek(x, t);
+      return true;
+    };
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      nx[t].start(x);
+      nx[t].seek(x, t);
+    }
+    bool ok = true;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (ok && nx[t].on && nx[t].n < ahead) ok = scores(t);
+    Walk w;
+    for (w.start(x); ok && w.on; w.next(x)) {
+      const int sv = w.n % VST;
+      const bool part = w.it.nk - w.j * BN < BN;
+      bool seen = false;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        nx[t].start(x);
-        nx[t].seek(x, t);
-      }
-      bool ok = true;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && nx[t].on && nx[t].n < ahead) ok = scores(t);
-      Walk w;
-      for (w.start(x); ok && w.on; w.next(x)) {
-        const int sv = w.n % VST;
-        const bool part = w.it.nk - w.j * BN < BN;
-        bool seen = false;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (ok && takes(x, w.it, t, w.j)) {
-            if (!seen) {  // V of this key tile
-              ok = mbar_wait(bar(B_VFULL + sv), (w.n / VST) & 1, ctl) && (!part || mbar_wait(bar(B_VFIX + sv), (fixes >> sv) & 1, ctl));
-              seen = true;
-              if (!ok) break;
-            }
-            // O_t += P_t V in two halves of 64 states, the first one while the softmax forms the second
-            const uint64_t vd = dadd(vd0, sv * KVBYTES);
-            const uint32_t dst = tmem + col_o(t), pa = tmem + col_s(t), par = np[t] & 1;
-            const bool first = w.j == (x.alt ? t : 0);
-            ok = mbar_wait(bar(B_PFULL + t), par, ctl);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_bf16_ts(dst, pa + 8 * k, dadd(vd, k * 16 * 128), ID_O, (first && k == 0) ? 0u : 1u);
-            mma_commit(bar(B_OHALF + t));
-            ok = mbar_wait(bar(B_PFULL2 + t), par, ctl);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 4; k < 8; ++k) mma_bf16_ts(dst, pa + 8 * k, dadd(vd, k * 16 * 128), ID_O, 1u);
-            mma_commit(bar(B_ODONE + t));
-            if (x.alt || t == 1 || !has_rows(x, w.it, 1)) mma_commit(bar(B_VEMPTY + sv));
-            ++np[t];
+        if (ok && takes(x, w.it, t, w.j)) {
+          if (!seen) {  // V of this key tile
+            ok = mbar_wait_warp(bar(B_VFULL + sv), (w.n / VST) & 1, ctl) &&
+                 (!part || mbar_wait_warp(bar(B_VFIX + sv), (fixes >> sv) & 1, ctl));
+            seen = true;
           }
-          // the tile's next scores, once its last ones are used up, and no further ahead than the ring reaches
-          if (ok && nx[t].on && ns[t] == np[t] && nx[t].n <= w.n + ahead) ok = scores(t);
+          // O_t += P_t V in two halves of 64 states, the first one while the softmax forms the second
+          const uint64_t vd = dadd(vd0, sv * KVBYTES);
+          const uint32_t dst = tmem + col_o(t), pa = tmem + col_s(t), par = np[t] & 1;
+          const bool first = w.j == (x.alt ? t : 0);
+          ok = ok && mbar_wait_warp(bar(B_PFULL + t), par, ctl);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_bf16_ts_w(dst, pa + 8 * k, dadd(vd, k * 16 * 128), ID_O, (first && k == 0) ? 0u : 1u, el);
+          mma_commit_w(bar(B_OHALF + t), el);
+          ok = mbar_wait_warp(bar(B_PFULL2 + t), par, ctl);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 4; k < 8; ++k) mma_bf16_ts_w(dst, pa + 8 * k, dadd(vd, k * 16 * 128), ID_O, 1u, el);
+          mma_commit_w(bar(B_ODONE + t), el);
+          if (x.alt || t == 1 || !has_rows(x, w.it, 1)) mma_commit_w(bar(B_VEMPTY + sv), el);
+          ++np[t];
         }
-        if (part) fixes ^= 1u << sv;
+        // the tile's next scores, once its last ones are used up, and no further ahead than the ring reaches
+        if (ok && nx[t].on && ns[t] == np[t] && nx[t].n <= w.n + ahead) ok = scores(t);
       }
-      mma_commit(bar(B_DRAIN));
-      mbar_drain(bar(B_DRAIN), 0);
+      if (part) fixes ^= 1u << sv;
     }
+    mma_commit_w(bar(B_DRAIN), el);
+    mbar_drain(bar(B_DRAIN), 0);
   } else {
     // ------------------------------------------------------------ softmax
     const int t = (warp - 4) >> 2;
@@ -357,8 +364,9 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
     const bool whole = (reinterpret_cast<uintptr_t>(x.y) & 31) == 0;
     int n = 0;  // key tiles of this tile so far
     bool ok = true;
-    for (int item = blockIdx.x; ok && item < x.items; item += gridDim.x) {
-      const Item it = decode(x, item);
+    ItemPos pos;
+    for (pos.start(x.grid); ok && pos.on(x.grid); pos.next(x.grid)) {
+      const Item it = decode(x, pos);
       if (!has_rows(x, it, t)) continue;
       float m_used = -INFINITY, l_sum = 0.f;
       bool any = false;
@@ -549,7 +557,7 @@ __global__ void __launch_bounds__(256) k_xattn_join(const XtDev x, int parts) {
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, x.po[(i * x.rows + row) * D + (D / 32) * lane + e], acc[e]);
   }
-  const int b = (int)(row / ((long long)x.Tq * x.H));
+  const int b = (int)(row / ((long long)x.Tq * x.H));  // one row a warp
   const bool none = valid_states(x, b) == 0;
   const float inv = none ? 0.f : 1.0f / s;
   uint32_t u[D / 64];
@@ -610,8 +618,9 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   XtDev x{};
   x.B = d.B; x.Tq = d.Tq; x.L = d.L; x.H = d.H; x.G = d.G;
-  x.P = c.P; x.TT = c.TT; x.HG = c.HG; x.pairs = c.pairs; x.ns = c.ns; x.alt = c.alt;
-  x.items = (int)c.items;
+  const unsigned grid = (unsigned)(c.items < kSms ? c.items : kSms);
+  x.P = c.P; x.TT = c.TT; x.ns = c.ns; x.alt = c.alt;
+  x.grid = item_grid((int)c.items, c.ns, c.pairs, c.HG, (int)grid);
   x.scale = d.scale;
   x.kv_len = d.kv_len;
   x.y = static_cast<__nv_bfloat16*>(const_cast<void*>(a.y));
@@ -625,7 +634,6 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)2 * BM * D * 2 + (size_t)(KST + VST) * BN * D * 2 + 40 * 8 + 16;
   cudaError_t e = cudaFuncSetAttribute(k_xattn_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)(c.items < kSms ? c.items : kSms);
   k_xattn_tc<D><<<grid, kThr, smem, s>>>(x, mq, mk, mv);
   if ((e = cudaGetLastError()) != cudaSuccess || !c.parts) return e;
   k_xattn_join<D><<<(unsigned)((x.rows + 7) / 8), 256, 0, s>>>(x, c.parts);
