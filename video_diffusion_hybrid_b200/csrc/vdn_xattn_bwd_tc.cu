@@ -48,8 +48,11 @@ constexpr int kSms = 148;
 
 struct XbDev {
   int B, Tq, L, H, Hkv, G;
-  int nqt, nkt;             // query tiles, key tiles (of L)
-  int ns, per, items;       // dq: splits of the key tiles; dkv: splits of G nqt query tiles, `per` each
+  int nqt;                  // query tiles
+  int ns, per;              // dq: splits of the key tiles; dkv: splits of G nqt query tiles, `per` each
+  // dq: splits, heads, query tiles, batch elements; dkv: key tiles, key heads, splits, batch elements.  CTAs that run
+  // at the same time so share the tokens: their heads' rows lie side by side in memory
+  ItemGrid grid;
   float scale;
   const int* kv_len;
   const float* lse;
@@ -61,9 +64,24 @@ struct XbDev {
 };
 
 __device__ __forceinline__ int valid_states(const XbDev& x, int b) {
-  if (x.kv_len == nullptr) return x.L;
-  const int n = __ldg(x.kv_len + b);
-  return n < 0 ? 0 : n > x.L ? x.L : n;
+  return x.kv_len == nullptr ? x.L : max(0, min(__ldg(x.kv_len + b), x.L));
+}
+// the same with b alike in the whole warp, the answer in a uniform register
+__device__ __forceinline__ int valid_states_warp(const XbDev& x, int b) {
+  return x.kv_len == nullptr ? x.L : __reduce_max_sync(0xffffffffu, valid_states(x, b));
+}
+
+// a read-only 16-byte load that stays where it is written (ahead of the work that hides its latency)
+__device__ __forceinline__ uint4 ldg_pinned(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ float ldg_pinned(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
 }
 
 // packed bf16 pairs of a 128-column tile: columns [64 h, 64 h + 64) as 32 packed columns from 64 h on
@@ -77,13 +95,12 @@ static __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorM
       : "memory");
 }
 
-// 16 floats as bf16: 32 bytes, 16-byte aligned
+// 16 floats as bf16: 32 bytes, a whole sector where the pointer allows it
 __device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, float f) {
   uint32_t u[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) u[i] = pack_bf16(v[2 * i] * f, v[2 * i + 1] * f);
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  store32(p, u, (reinterpret_cast<uintptr_t>(p) & 31) == 0);
 }
 
 // 32 columns of an accumulator row (times f) to a bf16 row or a partial sum
@@ -98,22 +115,22 @@ __device__ __forceinline__ void emit32(__nv_bfloat16* o, float* part, long long 
   }
 }
 
-// D(128 x 128) = A(128 x D) B(128 x D)^T, both K-major in 64-column blocks
+// D(128 x 128) = A(128 x D) B(128 x D)^T, both K-major in 64-column blocks; by a converged warp, `el` its elected lane
 template <int D>
-__device__ __forceinline__ void gemm_t(uint32_t dst, uint64_t a, uint64_t b) {
+__device__ __forceinline__ void gemm_t(uint32_t dst, uint64_t a, uint64_t b, uint32_t el) {
   constexpr uint32_t ID = idesc_bf16(BR, BR, false);
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
     const uint32_t off = (k >> 2) * (BR * 128) + (k & 3) * 32;
-    mma_bf16(dst, dadd(a, off), dadd(b, off), ID, k > 0 ? 1u : 0u);
+    mma_bf16_w(dst, dadd(a, off), dadd(b, off), ID, k > 0 ? 1u : 0u, el);
   }
 }
 // D(128 x D) (+)= A(TMEM, 128 x 128 packed) B(128 x D, MN-major)
 template <int D>
-__device__ __forceinline__ void gemm_ts(uint32_t dst, uint32_t a, uint64_t b, bool first) {
+__device__ __forceinline__ void gemm_ts(uint32_t dst, uint32_t a, uint64_t b, bool first, uint32_t el) {
   constexpr uint32_t ID = idesc_bf16(BR, D, true);
 #pragma unroll
-  for (int k = 0; k < BR / 16; ++k) mma_bf16_ts(dst, a + pk_k(k), dadd(b, k * 16 * 128), ID, (first && k == 0) ? 0u : 1u);
+  for (int k = 0; k < BR / 16; ++k) mma_bf16_ts_w(dst, a + pk_k(k), dadd(b, k * 16 * 128), ID, (first && k == 0) ? 0u : 1u, el);
 }
 
 // -------------------------------------------------------------------- dq --
@@ -121,35 +138,39 @@ struct QItem {
   int b, h, q0, sp;   // q0: first token of the tile within its batch element
   int k0, nk, nt;     // first state (over all batch elements), valid states, key tiles
 };
-__device__ __forceinline__ QItem decode_q(const XbDev& x, int item) {
+__device__ __forceinline__ QItem decode_q(const XbDev& x, const ItemPos& p) {
   QItem t;
-  t.sp = item % x.ns;
-  int r = item / x.ns;
-  t.q0 = (r % x.nqt) * BR;
-  r /= x.nqt;
-  t.h = r % x.H;
-  t.b = r / x.H;
-  const int n = valid_states(x, t.b), all = (n + BR - 1) / BR, per = (all + x.ns - 1) / x.ns;
-  const int lo = min(t.sp * per, all), hi = min(lo + per, all);
+  t.sp = p.d0;
+  t.h = p.d1;
+  t.q0 = p.d2 * BR;
+  t.b = p.d3;
+  const int n = valid_states_warp(x, t.b), all = (n + BR - 1) / BR;
+  int lo = 0, hi = all;
+  if (x.ns > 1) {
+    const int per = (all + x.ns - 1) / x.ns;
+    lo = min(t.sp * per, all);
+    hi = min(lo + per, all);
+  }
   t.nt = hi - lo;
   t.k0 = t.b * x.L + lo * BR;
   t.nk = min(n, hi * BR) - lo * BR;
   return t;
 }
-// a CTA's key tiles in order, `n` counting them over its items and `i` the items that have any
+// a CTA's key tiles in order, `n` counting them over its items and `i` the items that have any (whole warps)
 struct QWalk {
-  int item, j, n, i;
+  ItemPos pos;
+  int j, n, i;
   bool on;
   QItem it;
   __device__ __forceinline__ void settle(const XbDev& x) {
-    for (; item < x.items; item += gridDim.x) {
-      it = decode_q(x, item);
+    for (; pos.on(x.grid); pos.next(x.grid)) {
+      it = decode_q(x, pos);
       if (it.nt > 0) return;
     }
     on = false;
   }
   __device__ __forceinline__ void start(const XbDev& x) {
-    item = blockIdx.x;
+    pos.start(x.grid);
     j = n = i = 0;
     on = true;
     settle(x);
@@ -159,7 +180,7 @@ struct QWalk {
     if (++j < it.nt) return;
     j = 0;
     ++i;
-    item += gridDim.x;
+    pos.next(x.grid);
     settle(x);
   }
   __device__ __forceinline__ bool last() const { return j + 1 == it.nt; }
@@ -258,101 +279,136 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
       for (int n = max(nk - VST, 0); n < nk; ++n) mbar_drain(bar(B_VFULL + n % VST), (n / VST) & 1);
     }
   } else if (warp == 1) {
-    // ---- MMA issuer
-    if (lane == 0) {
-      const uint64_t qd = sdesc(smem_u32(sQ), 16, 1024), od = sdesc(smem_u32(sO), 16, 1024);
-      const uint64_t kd = sdesc(smem_u32(sK), 16, 1024), vd = sdesc(smem_u32(sV), 16, 1024);
-      const uint64_t kmn = sdesc(smem_u32(sK), BR * 128, 1024);  // K as the MN-major B of dQ += dS K
-      QWalk ws, wp, w;  // scores, dP, dQ
-      ws.start(x);
-      wp.start(x);
-      w.start(x);
-      uint32_t fixes = 0;
-      auto scores = [&]() -> bool {
-        const int sk = ws.n % KST;
-        if (ws.j == 0 && !mbar_wait(bar(B_QFULL), ws.i & 1, ctl)) return false;
-        if (!mbar_wait(bar(B_KFULL + sk), (ws.n / KST) & 1, ctl)) return false;
-        if (ws.it.nk - ws.j * BR < BR) {
-          if (!mbar_wait(bar(B_KFIX + sk), (fixes >> sk) & 1, ctl)) return false;
-          fixes ^= 1u << sk;
-        }
-        tc_fence_after();
-        gemm_t<D>(tmem + COL_S + 128 * (ws.n & 1), qd, dadd(kd, sk * TILE));
-        mma_commit(bar(B_SFULL + (ws.n & 1)));
-        if (ws.last()) mma_commit(bar(B_QEMPTY));
-        ws.next(x);
-        return true;
-      };
-      auto dprod = [&]() -> bool {
-        const int sv = wp.n % VST;
-        if (wp.j == 0 && !mbar_wait(bar(B_OFULL), wp.i & 1, ctl)) return false;
-        if (!mbar_wait(bar(B_VFULL + sv), (wp.n / VST) & 1, ctl)) return false;
-        tc_fence_after();
-        gemm_t<D>(tmem + COL_P, od, dadd(vd, sv * TILE));
-        mma_commit(bar(B_PFULL));
-        mma_commit(bar(B_VEMPTY + sv));
-        if (wp.last()) mma_commit(bar(B_OEMPTY));
-        wp.next(x);
-        return true;
-      };
-      bool ok = !ws.on || (scores() && dprod() && (!ws.on || scores()));
-      for (; ok && w.on; w.next(x)) {
-        ok = mbar_wait(bar(B_DS), w.n & 1, ctl);
-        if (!ok) break;
-        tc_fence_after();
-        if (wp.on && !(ok = dprod())) break;
-        gemm_ts<D>(tmem + COL_Q, tmem + COL_S + 128 * (w.n & 1), dadd(kmn, (w.n % KST) * TILE), w.j == 0);
-        mma_commit(bar(B_KEMPTY + w.n % KST));
-        if (w.last()) mma_commit(bar(B_ACC));
-        if (ws.on) ok = scores();  // over the buffer whose dS the product above reads first
+    // ---- MMA issuer (the whole warp, converged; one elected lane issues)
+    const uint32_t el = elect_one();
+    const uint64_t qd = sdesc(smem_u32(sQ), 16, 1024), od = sdesc(smem_u32(sO), 16, 1024);
+    const uint64_t kd = sdesc(smem_u32(sK), 16, 1024), vd = sdesc(smem_u32(sV), 16, 1024);
+    const uint64_t kmn = sdesc(smem_u32(sK), BR * 128, 1024);  // K as the MN-major B of dQ += dS K
+    QWalk ws, wp, w;  // scores, dP, dQ
+    ws.start(x);
+    wp.start(x);
+    w.start(x);
+    uint32_t fixes = 0;  // a bit for each K stage: parity of its next hand-over by the producer's zeroing
+    auto scores = [&]() -> bool {
+      const int sk = ws.n % KST;
+      if (ws.j == 0 && !mbar_wait_warp(bar(B_QFULL), ws.i & 1, ctl)) return false;
+      if (!mbar_wait_warp(bar(B_KFULL + sk), (ws.n / KST) & 1, ctl)) return false;
+      if (ws.it.nk - ws.j * BR < BR) {
+        if (!mbar_wait_warp(bar(B_KFIX + sk), (fixes >> sk) & 1, ctl)) return false;
+        fixes ^= 1u << sk;
       }
-      mma_commit(bar(B_DRAIN));
-      mbar_drain(bar(B_DRAIN), 0);
+      tc_fence_after();
+      gemm_t<D>(tmem + COL_S + 128 * (ws.n & 1), qd, dadd(kd, sk * TILE), el);
+      mma_commit_w(bar(B_SFULL + (ws.n & 1)), el);
+      if (ws.last()) mma_commit_w(bar(B_QEMPTY), el);
+      ws.next(x);
+      return true;
+    };
+    auto dprod = [&]() -> bool {
+      const int sv = wp.n % VST;
+      if (wp.j == 0 && !mbar_wait_warp(bar(B_OFULL), wp.i & 1, ctl)) return false;
+      if (!mbar_wait_warp(bar(B_VFULL + sv), (wp.n / VST) & 1, ctl)) return false;
+      tc_fence_after();
+      gemm_t<D>(tmem + COL_P, od, dadd(vd, sv * TILE), el);
+      mma_commit_w(bar(B_PFULL), el);
+      mma_commit_w(bar(B_VEMPTY + sv), el);
+      if (wp.last()) mma_commit_w(bar(B_OEMPTY), el);
+      wp.next(x);
+      return true;
+    };
+    bool ok = !ws.on || (scores() && dprod() && (!ws.on || scores()));
+    for (; ok && w.on; w.next(x)) {
+      ok = mbar_wait_warp(bar(B_DS), w.n & 1, ctl);
+      if (!ok) break;
+      tc_fence_after();
+      if (wp.on && !(ok = dprod())) break;
+      gemm_ts<D>(tmem + COL_Q, tmem + COL_S + 128 * (w.n & 1), dadd(kmn, (w.n % KST) * TILE), w.j == 0, el);
+      mma_commit_w(bar(B_KEMPTY + w.n % KST), el);
+      if (w.last()) mma_commit_w(bar(B_ACC), el);
+      if (ws.on) ok = scores();  // over the buffer whose dS the product above reads first
     }
+    mma_commit_w(bar(B_DRAIN), el);
+    mbar_drain(bar(B_DRAIN), 0);
   } else if (warp < 4) {
     // ---- row statistics: Delta = <dO, o> (kept for the other kernel too) and lse
-    constexpr int LR = D / 8, RW = 32 / LR;  // lanes a row, rows a step
+    // LR lanes a row with 16 bytes each; a batch of rows is loaded while the one before it is worked on, across items
+    // too (with one batch at a time the loads' latency made this the slowest role: 20,000 cycles an item).
+    constexpr int LR = D / 8, RW = 32 / LR, U = 8, NBATCH = BR / 2 / (RW * U);
     const int li = lane % LR, r0 = (warp - 2) * (BR / 2) + lane / LR;
-    int n = 0;
-    for (int item = blockIdx.x; item < x.items; item += gridDim.x) {
-      const QItem it = decode_q(x, item);
-      if (it.nt == 0) continue;
-      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_STEMPTY), (n - 1) & 1, ctl))) break;
+    uint4 a[2][U], g[2][U];
+    auto load = [&](int buf, const QItem& it, int batch) {
       const long long row0 = ((long long)it.b * x.Tq + it.q0) * x.H + it.h;
-      constexpr int U = 8;
-#pragma unroll 1
-      for (int r = 0; r < BR / 2; r += RW * U) {
-        uint4 a[U], g[U];
-        float lse[U];
+      const int most = x.Tq - 1 - it.q0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int rr = r0 + r + u * RW;
-          const bool on = it.q0 + rr < x.Tq;
-          const long long row = row0 + (long long)rr * x.H;
-          a[u] = on ? __ldg(reinterpret_cast<const uint4*>(x.y + row * D) + li) : make_uint4(0, 0, 0, 0);
-          g[u] = on ? __ldg(reinterpret_cast<const uint4*>(x.dy + row * D) + li) : make_uint4(0, 0, 0, 0);
-          lse[u] = on ? __ldg(x.lse + row) : INFINITY;  // rows past Tq: weight zero
+      for (int u = 0; u < U; ++u) {
+        // rows past Tq read the last one (loads without branches), and count for nothing below
+        const long long row = row0 + (long long)min(r0 + (batch * U + u) * RW, most) * x.H;
+        a[buf][u] = ldg_pinned(reinterpret_cast<const uint4*>(x.y + row * D) + li);
+        g[buf][u] = ldg_pinned(reinterpret_cast<const uint4*>(x.dy + row * D) + li);
+      }
+    };
+    float ls[2];  // lse of the rows lane and 32 + lane of this warp
+    auto load_lse = [&](const QItem& it) {
+      const float* p = x.lse + ((long long)it.b * x.Tq + it.q0) * x.H + it.h;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        ls[i] = ldg_pinned(p + (long long)min((warp - 2) * (BR / 2) + 32 * i + lane, x.Tq - 1 - it.q0) * x.H);
+    };
+    QWalk w;
+    w.start(x);
+    if (w.on) {
+      load(0, w.it, 0);
+      load_lse(w.it);
+    }
+    bool ok = true;
+    while (ok && w.on) {
+      const QItem it = w.it;
+      const int n = w.i;
+      w.j = it.nt - 1;
+      w.next(x);
+      const long long row0 = ((long long)it.b * x.Tq + it.q0) * x.H + it.h;
+#pragma unroll
+      for (int batch = 0; batch < NBATCH; ++batch) {
+        const int buf = batch & 1;
+        if (batch + 1 < NBATCH) load(buf ^ 1, it, batch + 1);
+        else if (w.on) load(buf ^ 1, w.it, 0);
+        if (batch == 0) {
+          if (n > 0 && !mbar_wait_warp(bar(B_STEMPTY), (n - 1) & 1, ctl)) { ok = false; break; }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = (warp - 2) * (BR / 2) + 32 * i + lane;
+            stat[rr].x = it.q0 + rr < x.Tq ? ls[i] * kLog2e : INFINITY;  // past Tq: weight zero
+          }
+          if (w.on) load_lse(w.it);
         }
+        float s[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const uint32_t av[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, gv[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
-          float s = 0.f;
+          const uint32_t av[4] = {a[buf][u].x, a[buf][u].y, a[buf][u].z, a[buf][u].w};
+          const uint32_t gv[4] = {g[buf][u].x, g[buf][u].y, g[buf][u].z, g[buf][u].w};
+          float lo = 0.f, hi = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s = fmaf(__uint_as_float(av[i] << 16), __uint_as_float(gv[i] << 16), s);
-            s = fmaf(__uint_as_float(av[i] & 0xFFFF0000u), __uint_as_float(gv[i] & 0xFFFF0000u), s);
+            lo = fmaf(__uint_as_float(av[i] << 16), __uint_as_float(gv[i] << 16), lo);
+            hi = fmaf(__uint_as_float(av[i] & 0xFFFF0000u), __uint_as_float(gv[i] & 0xFFFF0000u), hi);
           }
+          s[u] = lo + hi;
+        }
 #pragma unroll
-          for (int o = LR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          const int rr = r0 + r + u * RW;
+        for (int o = LR / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int rr = r0 + (batch * U + u) * RW;
           if (li == 0) {
-            stat[rr] = make_float2(lse[u] * kLog2e, s);
-            if (it.sp == 0 && it.q0 + rr < x.Tq) x.delta[row0 + (long long)rr * x.H] = s;
+            const bool on = it.q0 + rr < x.Tq;
+            stat[rr].y = on ? s[u] : 0.f;
+            if (it.sp == 0 && on) x.delta[row0 + (long long)rr * x.H] = s[u];
           }
         }
       }
-      mbar_arrive_warp(bar(B_STFULL));
-      ++n;
+      if (ok) mbar_arrive_warp(bar(B_STFULL));
     }
   } else {
     // ---- softmax
@@ -377,8 +433,9 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
       return true;
     };
     const long long rows = (long long)x.B * x.Tq * x.H;
-    for (int item = blockIdx.x; ok && item < x.items; item += gridDim.x) {
-      const QItem it = decode_q(x, item);
+    ItemPos pos;
+    for (pos.start(x.grid); ok && pos.on(x.grid); pos.next(x.grid)) {
+      const QItem it = decode_q(x, pos);
       const bool valid = it.q0 + row < x.Tq;
       const long long orow = ((long long)it.b * x.Tq + it.q0 + row) * x.H + it.h + (x.part != nullptr ? it.sp * rows : 0);
       if (it.nt == 0) {  // no states: dq is zero (a split without states leaves nothing)
@@ -399,19 +456,19 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_SFULL + (n & 1)), (n >> 1) & 1, ctl))) { ok = false; break; }
         tc_fence_after();
         float p[64];
-        {
-          float v[32];
+        tmem_ld32(sb, *reinterpret_cast<float(*)[32]>(p));
+        tmem_ld32(sb + 32, *reinterpret_cast<float(*)[32]>(p + 32));
+        tmem_wait_ld();
+        const float2 c2 = make_float2(c, c), nl2 = make_float2(-st.x, -st.x), nd2 = make_float2(-st.y, -st.y);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            tmem_ld32(sb + 32 * q, v);
-            tmem_wait_ld();
+        for (int i = 0; i < 64; i += 2) {
+          const float2 e = fma2(make_float2(p[i], p[i + 1]), c2, nl2);
+          p[i] = ex2(e.x);
+          p[i + 1] = ex2(e.y);
+        }
+        if (kv < 64) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) p[32 * q + i] = ex2(fmaf(v[i], c, -st.x));
-          }
-          if (kv < 64) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) p[i] = i < kv ? p[i] : 0.f;
-          }
+          for (int i = 0; i < 64; ++i) p[i] = i < kv ? p[i] : 0.f;
         }
         if (pend) {
           if (!emit()) { ok = false; break; }
@@ -431,8 +488,10 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
               for (int i = 0; i < 32; ++i) v[i] = 32 * q + i < kv ? v[i] : 0.f;  // what V holds there may be NaN
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              pk[16 * q + i] = __uint_as_float(pack_bf16(p[32 * q + 2 * i] * (v[2 * i] - st.y), p[32 * q + 2 * i + 1] * (v[2 * i + 1] - st.y)));
+            for (int i = 0; i < 16; ++i) {
+              const float2 d = mul2(make_float2(p[32 * q + 2 * i], p[32 * q + 2 * i + 1]), add2(make_float2(v[2 * i], v[2 * i + 1]), nd2));
+              pk[16 * q + i] = __uint_as_float(pack_bf16(d.x, d.y));
+            }
           }
         }
         tmem_st32(sb, pk);  // over this half's own scores
@@ -459,47 +518,55 @@ struct KItem {
   int b, hk, k0, sp;   // k0: first state of the tile within its batch element
   int lo, nt;          // first and number of its query tiles, counted over the group's heads
 };
-__device__ __forceinline__ KItem decode_k(const XbDev& x, int item) {
+__device__ __forceinline__ KItem decode_k(const XbDev& x, const ItemPos& p) {
   KItem t;
-  t.sp = item % x.ns;
-  int r = item / x.ns;
-  t.k0 = (r % x.nkt) * BR;
-  r /= x.nkt;
-  t.hk = r % x.Hkv;
-  t.b = r / x.Hkv;
+  t.k0 = p.d0 * BR;
+  t.hk = p.d1;
+  t.sp = p.d2;
+  t.b = p.d3;
   const int all = x.G * x.nqt;
   t.lo = min(t.sp * x.per, all);
-  t.nt = t.k0 < valid_states(x, t.b) ? min(x.per, all - t.lo) : 0;
+  t.nt = t.k0 < valid_states_warp(x, t.b) ? min(x.per, all - t.lo) : 0;
   return t;
 }
+// a CTA's query tiles in order; g and q: head of the group and query tile (whole warps)
 struct KWalk {
-  int item, j, n, i;
+  ItemPos pos;
+  int j, n, i, g, q;
   bool on;
   KItem it;
   __device__ __forceinline__ void settle(const XbDev& x) {
-    for (; item < x.items; item += gridDim.x) {
-      it = decode_k(x, item);
-      if (it.nt > 0) return;
+    for (; pos.on(x.grid); pos.next(x.grid)) {
+      it = decode_k(x, pos);
+      if (it.nt > 0) {
+        g = it.lo / x.nqt;
+        q = it.lo % x.nqt;
+        return;
+      }
     }
     on = false;
   }
   __device__ __forceinline__ void start(const XbDev& x) {
-    item = blockIdx.x;
+    pos.start(x.grid);
     j = n = i = 0;
     on = true;
     settle(x);
   }
   __device__ __forceinline__ void next(const XbDev& x) {
     ++n;
+    if (++q == x.nqt) {
+      q = 0;
+      ++g;
+    }
     if (++j < it.nt) return;
     j = 0;
     ++i;
-    item += gridDim.x;
+    pos.next(x.grid);
     settle(x);
   }
   __device__ __forceinline__ bool last() const { return j + 1 == it.nt; }
-  __device__ __forceinline__ int head(const XbDev& x) const { return it.hk * x.G + (it.lo + j) / x.nqt; }
-  __device__ __forceinline__ int tok(const XbDev& x) const { return (it.lo + j) % x.nqt * BR; }
+  __device__ __forceinline__ int head(const XbDev& x) const { return it.hk * x.G + g; }
+  __device__ __forceinline__ int tok() const { return q * BR; }
 };
 
 constexpr int kQst = 3, kOst = 2;
@@ -523,8 +590,8 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
   unsigned char* sV = sK + TILE;
   unsigned char* sQ = sV + TILE;
   unsigned char* sO = sQ + QST * TILE;
-  float2* stat = reinterpret_cast<float2*>(sO + OST * TILE);  // [2][BR] (lse in log2 units, Delta) of a tile's query rows
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stat + 2 * BR);
+  float* stat = reinterpret_cast<float*>(sO + OST * TILE);  // [2][2][BR] -lse (log2 units) and -Delta of a tile's query rows
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stat + 4 * BR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   if ((smem_u32(sm) & 1023u) != 0) {  // uniform
@@ -552,34 +619,42 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
 
   if (warp == 0) {
     // ---- producer: K and V of an item, the Q and dO rings
-    if (lane == 0) {
-      KWalk w;
-      int ni = 0, nq = 0;
-      for (w.start(x); w.on; w.next(x)) {
-        const int sq = w.n % QST, so = w.n % OST, h = w.head(x), t0 = w.tok(x);
-        if (w.j == 0) {
-          if (w.i > 0 && !mbar_wait(bar(B_KEMPTY), (w.i - 1) & 1, ctl)) break;
+    KWalk w;
+    int ni = 0, nq = 0;
+    for (w.start(x); w.on; w.next(x)) {
+      const int sq = w.n % QST, so = w.n % OST, h = w.head(x), t0 = w.tok();
+      if (w.j == 0) {
+        if (w.i > 0 && !mbar_wait_warp(bar(B_KEMPTY), (w.i - 1) & 1, ctl)) break;
+        if (lane == 0) {
           mbar_expect_tx(bar(B_KFULL), TILE);
           for (int c = 0; c < NB; ++c)
             tma_load_3d(smem_u32(sK + c * BR * 128), &tmk, bar(B_KFULL), c * 64, w.it.hk, w.it.b * x.L + w.it.k0);
-          ni = w.i + 1;
         }
-        if (w.n >= QST && !mbar_wait(bar(B_QEMPTY + sq), (w.n / QST - 1) & 1, ctl)) break;
+        ni = w.i + 1;
+      }
+      if (w.n >= QST && !mbar_wait_warp(bar(B_QEMPTY + sq), (w.n / QST - 1) & 1, ctl)) break;
+      if (lane == 0) {
         mbar_expect_tx(bar(B_QFULL + sq), TILE);
         for (int c = 0; c < NB; ++c)
           tma_load_4d(smem_u32(sQ + sq * TILE + c * BR * 128), &tmq, bar(B_QFULL + sq), c * 64, h, t0, w.it.b);
-        nq = w.n + 1;
-        if (w.j == 0) {
-          if (w.i > 0 && !mbar_wait(bar(B_VEMPTY), (w.i - 1) & 1, ctl)) break;
+      }
+      nq = w.n + 1;
+      if (w.j == 0) {
+        if (w.i > 0 && !mbar_wait_warp(bar(B_VEMPTY), (w.i - 1) & 1, ctl)) break;
+        if (lane == 0) {
           mbar_expect_tx(bar(B_VFULL), TILE);
           for (int c = 0; c < NB; ++c)
             tma_load_3d(smem_u32(sV + c * BR * 128), &tmv, bar(B_VFULL), c * 64, w.it.hk, w.it.b * x.L + w.it.k0);
         }
-        if (w.n >= OST && !mbar_wait(bar(B_OEMPTY + so), (w.n / OST - 1) & 1, ctl)) break;
+      }
+      if (w.n >= OST && !mbar_wait_warp(bar(B_OEMPTY + so), (w.n / OST - 1) & 1, ctl)) break;
+      if (lane == 0) {
         mbar_expect_tx(bar(B_OFULL + so), TILE);
         for (int c = 0; c < NB; ++c)
           tma_load_4d(smem_u32(sO + so * TILE + c * BR * 128), &tmdo, bar(B_OFULL + so), c * 64, h, t0, w.it.b);
       }
+    }
+    if (lane == 0) {
       if (ni > 0) mbar_drain(bar(B_KFULL), (ni - 1) & 1);
       if (ni > 0) mbar_drain(bar(B_VFULL), (ni - 1) & 1);
       for (int n = max(nq - QST, 0); n < nq; ++n) mbar_drain(bar(B_QFULL + n % QST), (n / QST) & 1);
@@ -587,79 +662,81 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
     }
   } else if (warp == 1) {
     // ---- MMA issuer
-    if (lane == 0) {
-      const uint64_t kd = sdesc(smem_u32(sK), 16, 1024), vd = sdesc(smem_u32(sV), 16, 1024);
-      const uint64_t qd = sdesc(smem_u32(sQ), 16, 1024), od = sdesc(smem_u32(sO), 16, 1024);
-      const uint64_t qmn = sdesc(smem_u32(sQ), BR * 128, 1024), omn = sdesc(smem_u32(sO), BR * 128, 1024);
-      KWalk ws, wp, w;
-      ws.start(x);
-      wp.start(x);
-      w.start(x);
-      auto scores = [&]() -> bool {  // S^T = K Q^T
-        const int sq = ws.n % QST;
-        if (ws.j == 0 && !mbar_wait(bar(B_KFULL), ws.i & 1, ctl)) return false;
-        if (!mbar_wait(bar(B_QFULL + sq), (ws.n / QST) & 1, ctl)) return false;
-        tc_fence_after();
-        gemm_t<D>(tmem + COL_S, kd, dadd(qd, sq * TILE));
-        mma_commit(bar(B_SFULL));
-        if (ws.last()) mma_commit(bar(B_KEMPTY));
-        ws.next(x);
-        return true;
-      };
-      auto dprod = [&]() -> bool {  // dP^T = V dO^T
-        const int so = wp.n % OST;
-        if (wp.j == 0 && !mbar_wait(bar(B_VFULL), wp.i & 1, ctl)) return false;
-        if (!mbar_wait(bar(B_OFULL + so), (wp.n / OST) & 1, ctl)) return false;
-        tc_fence_after();
-        gemm_t<D>(tmem + COL_P, vd, dadd(od, so * TILE));
-        mma_commit(bar(B_PFULL));
-        if (wp.last()) mma_commit(bar(B_VEMPTY));
-        wp.next(x);
-        return true;
-      };
-      bool ok = !ws.on || (scores() && dprod());
-      for (; ok && w.on; w.next(x)) {
-        ok = mbar_wait(bar(B_P), w.n & 1, ctl);
-        if (!ok) break;
-        tc_fence_after();
-        gemm_ts<D>(tmem + COL_V, tmem + COL_S, dadd(omn, (w.n % OST) * TILE), w.j == 0);  // dV += P^T dO
-        mma_commit(bar(B_OEMPTY + w.n % OST));
-        if (ws.on && !(ok = scores())) break;  // over P^T, which the product above reads first
-        ok = mbar_wait(bar(B_DS), w.n & 1, ctl);
-        if (!ok) break;
-        tc_fence_after();
-        gemm_ts<D>(tmem + COL_K, tmem + COL_P, dadd(qmn, (w.n % QST) * TILE), w.j == 0);  // dK += dS^T Q
-        mma_commit(bar(B_QEMPTY + w.n % QST));
-        if (w.last()) mma_commit(bar(B_ACC));
-        if (wp.on) ok = dprod();
-      }
-      mma_commit(bar(B_DRAIN));
-      mbar_drain(bar(B_DRAIN), 0);
+    const uint32_t el = elect_one();
+    const uint64_t kd = sdesc(smem_u32(sK), 16, 1024), vd = sdesc(smem_u32(sV), 16, 1024);
+    const uint64_t qd = sdesc(smem_u32(sQ), 16, 1024), od = sdesc(smem_u32(sO), 16, 1024);
+    const uint64_t qmn = sdesc(smem_u32(sQ), BR * 128, 1024), omn = sdesc(smem_u32(sO), BR * 128, 1024);
+    KWalk ws, wp, w;
+    ws.start(x);
+    wp.start(x);
+    w.start(x);
+    auto scores = [&]() -> bool {  // S^T = K Q^T
+      const int sq = ws.n % QST;
+      if (ws.j == 0 && !mbar_wait_warp(bar(B_KFULL), ws.i & 1, ctl)) return false;
+      if (!mbar_wait_warp(bar(B_QFULL + sq), (ws.n / QST) & 1, ctl)) return false;
+      tc_fence_after();
+      gemm_t<D>(tmem + COL_S, kd, dadd(qd, sq * TILE), el);
+      mma_commit_w(bar(B_SFULL), el);
+      if (ws.last()) mma_commit_w(bar(B_KEMPTY), el);
+      ws.next(x);
+      return true;
+    };
+    auto dprod = [&]() -> bool {  // dP^T = V dO^T
+      const int so = wp.n % OST;
+      if (wp.j == 0 && !mbar_wait_warp(bar(B_VFULL), wp.i & 1, ctl)) return false;
+      if (!mbar_wait_warp(bar(B_OFULL + so), (wp.n / OST) & 1, ctl)) return false;
+      tc_fence_after();
+      gemm_t<D>(tmem + COL_P, vd, dadd(od, so * TILE), el);
+      mma_commit_w(bar(B_PFULL), el);
+      if (wp.last()) mma_commit_w(bar(B_VEMPTY), el);
+      wp.next(x);
+      return true;
+    };
+    bool ok = !ws.on || (scores() && dprod());
+    for (; ok && w.on; w.next(x)) {
+      ok = mbar_wait_warp(bar(B_P), w.n & 1, ctl);
+      if (!ok) break;
+      tc_fence_after();
+      gemm_ts<D>(tmem + COL_V, tmem + COL_S, dadd(omn, (w.n % OST) * TILE), w.j == 0, el);  // dV += P^T dO
+      mma_commit_w(bar(B_OEMPTY + w.n % OST), el);
+      if (ws.on && !(ok = scores())) break;  // over P^T, which the product above reads first
+      ok = mbar_wait_warp(bar(B_DS), w.n & 1, ctl);
+      if (!ok) break;
+      tc_fence_after();
+      gemm_ts<D>(tmem + COL_K, tmem + COL_P, dadd(qmn, (w.n % QST) * TILE), w.j == 0, el);  // dK += dS^T Q
+      mma_commit_w(bar(B_QEMPTY + w.n % QST), el);
+      if (w.last()) mma_commit_w(bar(B_ACC), el);
+      if (wp.on) ok = dprod();
     }
+    mma_commit_w(bar(B_DRAIN), el);
+    mbar_drain(bar(B_DRAIN), 0);
   } else if (warp == 2) {
     // ---- the query rows' statistics, two tiles ahead
     KWalk w;
     for (w.start(x); w.on; w.next(x)) {
-      const int s = w.n & 1, t0 = w.tok(x);
+      const int s = w.n & 1, t0 = w.tok();
       const long long row0 = ((long long)w.it.b * x.Tq + t0) * x.H + w.head(x);
       float2 v[BR / 32];
 #pragma unroll
       for (int i = 0; i < BR / 32; ++i) {
         const int r = lane + 32 * i;
         const bool on = t0 + r < x.Tq;
-        v[i].x = on ? __ldg(x.lse + row0 + (long long)r * x.H) * kLog2e : INFINITY;  // 2^(s c - inf) = 0: no weight
-        v[i].y = on ? __ldg(x.delta + row0 + (long long)r * x.H) : 0.f;
+        v[i].x = on ? __ldg(x.lse + row0 + (long long)r * x.H) * -kLog2e : -INFINITY;  // 2^(s c - inf) = 0: no weight
+        v[i].y = on ? -__ldg(x.delta + row0 + (long long)r * x.H) : 0.f;
       }
       if (w.n >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar(B_STEMPTY + s), (w.n / 2 - 1) & 1, ctl))) break;
 #pragma unroll
-      for (int i = 0; i < BR / 32; ++i) stat[s * BR + lane + 32 * i] = v[i];
+      for (int i = 0; i < BR / 32; ++i) {
+        stat[2 * s * BR + lane + 32 * i] = v[i].x;
+        stat[(2 * s + 1) * BR + lane + 32 * i] = v[i].y;
+      }
       mbar_arrive_warp(bar(B_STFULL + s));
     }
   } else if (warp >= 4) {
     // ---- softmax: lane = state, columns = query rows
     const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
-    const float c = x.scale * kLog2e;
+    const float2 c2 = make_float2(x.scale * kLog2e, x.scale * kLog2e);
     bool ok = true, pend = false, pin = false, plive = false;
     int n = 0, ni = 0;
     long long prow = 0;  // the pending output's row; pin: inside L; plive: inside kv_len
@@ -689,8 +766,9 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
       return true;
     };
     const long long rows = (long long)x.B * x.L * x.Hkv;
-    for (int item = blockIdx.x; ok && item < x.items; item += gridDim.x) {
-      const KItem it = decode_k(x, item);
+    ItemPos pos;
+    for (pos.start(x.grid); ok && pos.on(x.grid); pos.next(x.grid)) {
+      const KItem it = decode_k(x, pos);
       const bool in = it.k0 + row < x.L, live = it.k0 + row < valid_states(x, it.b);
       const long long orow = ((long long)it.b * x.L + it.k0 + row) * x.Hkv + it.hk + (x.part != nullptr ? it.sp * rows : 0);
       if (it.nt == 0) {  // past the last state (or no rows in this split, which leaves nothing): zeros
@@ -707,24 +785,28 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
         continue;
       }
       for (int j = 0; j < it.nt; ++j, ++n) {
-        const float2* st = stat + (n & 1) * BR + 64 * half;
+        const float4* nl = reinterpret_cast<const float4*>(stat + 2 * (n & 1) * BR + 64 * half);
+        const float4* nd = nl + BR / 4;
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_STFULL + (n & 1)), (n >> 1) & 1, ctl) && mbar_wait(bar(B_SFULL), n & 1, ctl))) {
           ok = false;
           break;
         }
         tc_fence_after();
         float p[64], pk[32];
-        {
-          float v[32];
+        tmem_ld32(la + COL_S + 64 * half, *reinterpret_cast<float(*)[32]>(p));
+        tmem_ld32(la + COL_S + 64 * half + 32, *reinterpret_cast<float(*)[32]>(p + 32));
+        tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            tmem_ld32(la + COL_S + 64 * half + 32 * q, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) p[32 * q + i] = ex2(fmaf(v[i], c, -st[32 * q + i].x));
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) pk[i] = __uint_as_float(pack_bf16(p[2 * i], p[2 * i + 1]));
+        for (int i = 0; i < 64; i += 4) {
+          const float4 l = nl[i / 4];
+          const float2 e = fma2(make_float2(p[i], p[i + 1]), c2, make_float2(l.x, l.y));
+          const float2 f = fma2(make_float2(p[i + 2], p[i + 3]), c2, make_float2(l.z, l.w));
+          p[i] = ex2(e.x);
+          p[i + 1] = ex2(e.y);
+          p[i + 2] = ex2(f.x);
+          p[i + 3] = ex2(f.y);
+          pk[i / 2] = __uint_as_float(pack_bf16(p[i], p[i + 1]));
+          pk[i / 2 + 1] = __uint_as_float(pack_bf16(p[i + 2], p[i + 3]));
         }
         if (pend) {
           if (!emit(false)) { ok = false; break; }
@@ -743,9 +825,14 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
             tmem_ld32(la + COL_P + 64 * half + 32 * q, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              pk[16 * q + i] = __uint_as_float(pack_bf16(p[32 * q + 2 * i] * (v[2 * i] - st[32 * q + 2 * i].y),
-                                                         p[32 * q + 2 * i + 1] * (v[2 * i + 1] - st[32 * q + 2 * i + 1].y)));
+            for (int i = 0; i < 32; i += 4) {
+              const float4 d = nd[8 * q + i / 4];
+              const float2 e = mul2(make_float2(p[32 * q + i], p[32 * q + i + 1]), add2(make_float2(v[i], v[i + 1]), make_float2(d.x, d.y)));
+              const float2 f =
+                  mul2(make_float2(p[32 * q + i + 2], p[32 * q + i + 3]), add2(make_float2(v[i + 2], v[i + 3]), make_float2(d.z, d.w)));
+              pk[16 * q + i / 2] = __uint_as_float(pack_bf16(e.x, e.y));
+              pk[16 * q + i / 2 + 1] = __uint_as_float(pack_bf16(f.x, f.y));
+            }
           }
         }
         tmem_st32(la + COL_P + 64 * half, pk);
@@ -858,7 +945,7 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   char* ws = static_cast<char*>(a.scratch);
   XbDev x{};
   x.B = d.B; x.Tq = d.Tq; x.L = d.L; x.H = d.H; x.Hkv = d.Hkv; x.G = d.G;
-  x.nqt = c.nqt; x.nkt = c.nkt;
+  x.nqt = c.nqt;
   x.scale = d.scale;
   x.kv_len = d.kv_len;
   x.lse = a.lse;
@@ -878,19 +965,20 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   // dq first: it forms Delta
   XbDev xq = x;
   xq.ns = c.qs;
-  xq.items = (int)qi;
+  const int qgrid = (int)(qi < kSms ? qi : kSms), kgrid = (int)(ki < kSms ? ki : kSms);
+  xq.grid = item_grid((int)qi, c.qs, d.H, c.nqt, qgrid);
   xq.part = c.qs > 1 ? reinterpret_cast<float*>(ws + c.dq) : nullptr;
-  k_xattn_dq_tc<D><<<(unsigned)(qi < kSms ? qi : kSms), kThr, smq, s>>>(xq, mq, mo, mk, mv);
+  k_xattn_dq_tc<D><<<qgrid, kThr, smq, s>>>(xq, mq, mo, mk, mv);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   XbDev xk = x;
   xk.ns = c.ks;
   xk.per = c.kper;
-  xk.items = (int)ki;
+  xk.grid = item_grid((int)ki, c.nkt, d.Hkv, c.ks, kgrid);
   if (c.ks > 1) {
     xk.part = reinterpret_cast<float*>(ws + c.dk);
     xk.part2 = reinterpret_cast<float*>(ws + c.dk + (c.bytes - c.dk) / 2);
   }
-  k_xattn_dkv_tc<D><<<(unsigned)(ki < kSms ? ki : kSms), kThr, smk, s>>>(xk, mq, mo, mk, mv);
+  k_xattn_dkv_tc<D><<<kgrid, kThr, smk, s>>>(xk, mq, mo, mk, mv);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (c.qs > 1) {
     k_xattn_join_dq<<<(unsigned)(((long long)d.B * d.Tq * d.H * D / 4 + 255) / 256), 256, 0, s>>>(xq, D);

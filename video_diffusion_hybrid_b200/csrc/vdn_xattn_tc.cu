@@ -30,8 +30,8 @@
 // The softmax takes a key tile in two halves of 64 states and keeps a row's
 // reference m while no weight exceeds 2^8 (checked by the half's sum), so O is
 // rescaled only when the maximum grew by more than 8 in exp2 units.  P is
-// rounded to bf16 for the product; the row sum adds the rounded values, so o
-// is an exact convex combination of the rows of V.
+// rounded to bf16 for the product (the operand's type: a relative 2^-8 at most
+// of each weight); the row sum adds the unrounded values in fp32.
 //
 // TMEM (512 columns): O_0 [0,128), O_1 [128,256), S_0 [256,384), S_1 [384,512);
 // P_t over the first 64 columns of S_t.  One thread issues every product, in
@@ -63,7 +63,8 @@ struct XtDev {
   int B, Tq, L, H, G;
   int P, TT;           // heads and tokens of a tile (P TT <= 128 rows)
   int ns, alt;         // splits of the states, tiles alternate over key tiles
-  ItemGrid grid;       // splits, tile pairs over the tokens, head groups, batch elements
+  ItemGrid grid;       // splits, head groups, tile pairs over the tokens, batch elements: CTAs that run at the
+                       // same time share the tokens, and their heads' rows lie side by side in memory
   float scale;
   const int* kv_len;
   __nv_bfloat16* y;
@@ -90,9 +91,9 @@ __device__ __forceinline__ int valid_states(const XtDev& x, int b) {
 __device__ __forceinline__ Item decode(const XtDev& x, const ItemPos& p) {
   Item t;
   t.sp = p.d0;
-  t.hg = p.d2;
+  t.hg = p.d1;
   t.b = p.d3;
-  const int first = p.d1 * (x.alt ? 1 : 2) * x.TT;
+  const int first = p.d2 * (x.alt ? 1 : 2) * x.TT;
   t.q0 = t.b * x.Tq + first;
   t.left = x.Tq - first;
   const int n = valid_states(x, t.b), all = (n + BN - 1) / BN;
@@ -145,26 +146,6 @@ struct Walk {
     while (on && !takes(x, it, t, j)) next(x);
   }
 };
-
-// lo and hi halves of a packed bf16 pair added exactly into two fp32 sums
-__device__ __forceinline__ void add_bf16x2_f32(float& s_lo, float& s_hi, uint32_t u) {
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.rn.f32.bf16 %0, lo, %0;\n\t"
-      "add.rn.f32.bf16 %1, hi, %1;\n\t}"
-      : "+f"(s_lo), "+f"(s_hi)
-      : "r"(u));
-}
-
-// 32 bytes, whole sectors (32-byte aligned), or two halves
-__device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8], bool whole) {
-  if (whole) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
-                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-  }
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThr, 1)
@@ -383,17 +364,17 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
           // A full half after the item's first: one pass with the reference kept, where the sum of P is at most 2^8
           if ((any || h == 1) && kvh >= 64) {
             const float2 c2 = make_float2(c, c), nmc2 = make_float2(-m_used * c, -m_used * c);
-            float ps[8];
+            float2 ps[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) ps[u] = 0.f;
+            for (int u = 0; u < 4; ++u) ps[u] = make_float2(0.f, 0.f);
             float pk[32];
             auto chunk = [&](const float (&v)[32], int o) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float2 e = fma2(make_float2(v[2 * i], v[2 * i + 1]), c2, nmc2);
-                const uint32_t u = pack_bf16(ex2(e.x), ex2(e.y));
-                add_bf16x2_f32(ps[2 * (i & 3)], ps[2 * (i & 3) + 1], u);
-                pk[o + i] = __uint_as_float(u);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                ps[i & 3] = add2(ps[i & 3], p);
+                pk[o + i] = __uint_as_float(pack_bf16(p.x, p.y));
               }
             };
             float va[32], vb[32];
@@ -403,7 +384,8 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
             chunk(va, 0);
             tmem_wait_ld();
             chunk(vb, 16);
-            const float psum = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+            const float2 pt = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
+            const float psum = pt.x + pt.y;
             if (!__any_sync(0xffffffffu, !(psum <= 256.0f))) {
               tmem_st32(scol + 32 * h, pk);
               l_sum += psum;
@@ -452,24 +434,25 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
             }
             // a row with no finite score so far takes the reference 0: weights of 0, not of inf - inf
             const float mc = m_used == -INFINITY ? 0.f : m_used * c;
-            float ps[8];
+            const float2 c2 = make_float2(c, c), nmc2 = make_float2(-mc, -mc);
+            float2 ps[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) ps[u] = 0.f;
+            for (int u = 0; u < 4; ++u) ps[u] = make_float2(0.f, 0.f);
             float pk[32];
+            auto chunk = [&](const float (&v)[32], int o) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t u = pack_bf16(ex2(fmaf(v0[2 * i], c, -mc)), ex2(fmaf(v0[2 * i + 1], c, -mc)));
-              add_bf16x2_f32(ps[2 * (i & 3)], ps[2 * (i & 3) + 1], u);
-              pk[i] = __uint_as_float(u);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t u = pack_bf16(ex2(fmaf(v1[2 * i], c, -mc)), ex2(fmaf(v1[2 * i + 1], c, -mc)));
-              add_bf16x2_f32(ps[2 * (i & 3)], ps[2 * (i & 3) + 1], u);
-              pk[16 + i] = __uint_as_float(u);
-            }
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = fma2(make_float2(v[2 * i], v[2 * i + 1]), c2, nmc2);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                ps[i & 3] = add2(ps[i & 3], p);
+                pk[o + i] = __uint_as_float(pack_bf16(p.x, p.y));
+              }
+            };
+            chunk(v0, 0);
+            chunk(v1, 16);
             tmem_st32(scol + 32 * h, pk);
-            l_sum += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+            const float2 pt = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
+            l_sum += pt.x + pt.y;
           }
           tmem_wait_st();
           tc_fence_before();
@@ -620,7 +603,7 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   x.B = d.B; x.Tq = d.Tq; x.L = d.L; x.H = d.H; x.G = d.G;
   const unsigned grid = (unsigned)(c.items < kSms ? c.items : kSms);
   x.P = c.P; x.TT = c.TT; x.ns = c.ns; x.alt = c.alt;
-  x.grid = item_grid((int)c.items, c.ns, c.pairs, c.HG, (int)grid);
+  x.grid = item_grid((int)c.items, c.ns, c.HG, c.pairs, (int)grid);
   x.scale = d.scale;
   x.kv_len = d.kv_len;
   x.y = static_cast<__nv_bfloat16*>(const_cast<void*>(a.y));
