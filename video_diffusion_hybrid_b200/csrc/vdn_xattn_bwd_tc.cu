@@ -8,7 +8,7 @@
 // partial sums are joined in a fixed order) and no atomics are needed:
 //
 //   k_xattn_dq_tc : 128 query rows of a head over its key tiles; three products
-//                   a tile (S = Q K^T, dP = dO V^T, dQ += dS K).  Forms Delta on the way.
+//                   a tile (S = Q K^T, dP = dO V^T, dQ += dS K).
 //   k_xattn_dkv_tc: 128 states of a key head over the query tiles of its group;
 //                   four products a tile (S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q).
 //
@@ -24,10 +24,9 @@
 // after P(j) the pipe has dV(j) and S(j+1), after dS(j) it has dK(j) and
 // dP(j+1), which run under the exponentials of P(j+1).
 //
-// Roles (384 threads): warp 0 TMA producer, warp 1 TMEM allocator and MMA
-// issuer, warps 2 (and 3) the rows' statistics, warps 4..11 softmax: two warps
-// for each TMEM lane quadrant (thread = lane = row), each with half of the
-// columns.
+// Roles (640 threads): warp 0 TMA producer, warp 1 TMEM allocator and MMA
+// issuer, warp 2 the rows' statistics, warps 4..19 softmax: four warps for each
+// TMEM lane quadrant (lane = row), each with a quarter of the columns.
 //
 // Nothing past kv_len is used: dq masks P and dS and zeroes those rows of K in
 // shared memory; in dkv they are rows of their own that are stored as zeros.
@@ -41,8 +40,8 @@ namespace {
 using namespace tc;
 
 constexpr int BR = 128;
-constexpr int kThr = 384;
-constexpr int kSoftWarps = 8;
+constexpr int kThr = 640;
+constexpr int kSoftWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSms = 148;
 
@@ -71,21 +70,28 @@ __device__ __forceinline__ int valid_states_warp(const XbDev& x, int b) {
   return x.kv_len == nullptr ? x.L : __reduce_max_sync(0xffffffffu, valid_states(x, b));
 }
 
-// a read-only 16-byte load that stays where it is written (ahead of the work that hides its latency)
-__device__ __forceinline__ uint4 ldg_pinned(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
+// packed bf16 pairs of a 128-column tile: columns [32 h, 32 h + 32) as 16 packed columns from 32 h on
+__host__ __device__ constexpr uint32_t pk_k(int k) { return 8u * (k & 1) + 32u * (k >> 1); }
 
-__device__ __forceinline__ float ldg_pinned(const float* p) {
-  float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-  return v;
+static __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-
-// packed bf16 pairs of a 128-column tile: columns [64 h, 64 h + 64) as 32 packed columns from 64 h on
-__host__ __device__ constexpr uint32_t pk_k(int k) { return 8u * k + 32u * (k >> 2); }
+static __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 
 static __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
   asm volatile(
@@ -103,15 +109,14 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, float 
   store32(p, u, (reinterpret_cast<uintptr_t>(p) & 31) == 0);
 }
 
-// 32 columns of an accumulator row (times f) to a bf16 row or a partial sum
-__device__ __forceinline__ void emit32(__nv_bfloat16* o, float* part, long long at, const float (&v)[32], float f) {
+// 16 columns of an accumulator row (times f) to a bf16 row or a partial sum
+__device__ __forceinline__ void emit16(__nv_bfloat16* o, float* part, long long at, const float (&v)[16], float f) {
   if (part != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 4)
+    for (int i = 0; i < 16; i += 4)
       *reinterpret_cast<float4*>(part + at + i) = make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
   } else {
     store16(o + at, v, f);
-    store16(o + at + 16, v + 16, f);
   }
 }
 
@@ -202,7 +207,7 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
   unsigned char* sO = sQ + TILE;
   unsigned char* sK = sO + TILE;
   unsigned char* sV = sK + KST * TILE;
-  float2* stat = reinterpret_cast<float2*>(sV + VST * TILE);  // [BR] (lse in log2 units, Delta) of the item's rows
+  float2* stat = reinterpret_cast<float2*>(sV + VST * TILE);  // [BR] (-lse in log2 units, -Delta) of the item's rows
   uint64_t* bars = reinterpret_cast<uint64_t*>(stat + BR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -211,7 +216,7 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
   const Ctl ctl{abort_flag, x.status, (unsigned)VDN_TAG_XATTN_BWD, 0};
   auto bar = [&](int i) { return smem_u32(bars + i); };
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i == B_DS || i == B_STEMPTY ? kSoftWarps : i == B_STFULL ? 2 : 1);
+    for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i == B_DS || i == B_STEMPTY ? kSoftWarps : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -329,105 +334,43 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
     }
     mma_commit_w(bar(B_DRAIN), el);
     mbar_drain(bar(B_DRAIN), 0);
-  } else if (warp < 4) {
-    // ---- row statistics: Delta = <dO, o> (kept for the other kernel too) and lse
-    // LR lanes a row with 16 bytes each; a batch of rows is loaded while the one before it is worked on, across items
-    // too (with one batch at a time the loads' latency made this the slowest role: 20,000 cycles an item).
-    constexpr int LR = D / 8, RW = 32 / LR, U = 8, NBATCH = BR / 2 / (RW * U);
-    const int li = lane % LR, r0 = (warp - 2) * (BR / 2) + lane / LR;
-    uint4 a[2][U], g[2][U];
-    auto load = [&](int buf, const QItem& it, int batch) {
-      const long long row0 = ((long long)it.b * x.Tq + it.q0) * x.H + it.h;
-      const int most = x.Tq - 1 - it.q0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // rows past Tq read the last one (loads without branches), and count for nothing below
-        const long long row = row0 + (long long)min(r0 + (batch * U + u) * RW, most) * x.H;
-        a[buf][u] = ldg_pinned(reinterpret_cast<const uint4*>(x.y + row * D) + li);
-        g[buf][u] = ldg_pinned(reinterpret_cast<const uint4*>(x.dy + row * D) + li);
-      }
-    };
-    float ls[2];  // lse of the rows lane and 32 + lane of this warp
-    auto load_lse = [&](const QItem& it) {
-      const float* p = x.lse + ((long long)it.b * x.Tq + it.q0) * x.H + it.h;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        ls[i] = ldg_pinned(p + (long long)min((warp - 2) * (BR / 2) + 32 * i + lane, x.Tq - 1 - it.q0) * x.H);
-    };
+  } else if (warp == 2) {
+    // ---- the rows' statistics, an item ahead
     QWalk w;
-    w.start(x);
-    if (w.on) {
-      load(0, w.it, 0);
-      load_lse(w.it);
-    }
-    bool ok = true;
-    while (ok && w.on) {
-      const QItem it = w.it;
-      const int n = w.i;
-      w.j = it.nt - 1;
-      w.next(x);
-      const long long row0 = ((long long)it.b * x.Tq + it.q0) * x.H + it.h;
+    for (w.start(x); w.on; w.next(x)) {
+      if (w.j > 0) continue;
+      const long long row0 = ((long long)w.it.b * x.Tq + w.it.q0) * x.H + w.it.h;
+      float2 v[BR / 32];
 #pragma unroll
-      for (int batch = 0; batch < NBATCH; ++batch) {
-        const int buf = batch & 1;
-        if (batch + 1 < NBATCH) load(buf ^ 1, it, batch + 1);
-        else if (w.on) load(buf ^ 1, w.it, 0);
-        if (batch == 0) {
-          if (n > 0 && !mbar_wait_warp(bar(B_STEMPTY), (n - 1) & 1, ctl)) { ok = false; break; }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int rr = (warp - 2) * (BR / 2) + 32 * i + lane;
-            stat[rr].x = it.q0 + rr < x.Tq ? ls[i] * kLog2e : INFINITY;  // past Tq: weight zero
-          }
-          if (w.on) load_lse(w.it);
-        }
-        float s[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t av[4] = {a[buf][u].x, a[buf][u].y, a[buf][u].z, a[buf][u].w};
-          const uint32_t gv[4] = {g[buf][u].x, g[buf][u].y, g[buf][u].z, g[buf][u].w};
-          float lo = 0.f, hi = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            lo = fmaf(__uint_as_float(av[i] << 16), __uint_as_float(gv[i] << 16), lo);
-            hi = fmaf(__uint_as_float(av[i] & 0xFFFF0000u), __uint_as_float(gv[i] & 0xFFFF0000u), hi);
-          }
-          s[u] = lo + hi;
-        }
-#pragma unroll
-        for (int o = LR / 2; o > 0; o >>= 1)
-#pragma unroll
-          for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int rr = r0 + (batch * U + u) * RW;
-          if (li == 0) {
-            const bool on = it.q0 + rr < x.Tq;
-            stat[rr].y = on ? s[u] : 0.f;
-            if (it.sp == 0 && on) x.delta[row0 + (long long)rr * x.H] = s[u];
-          }
-        }
+      for (int i = 0; i < BR / 32; ++i) {
+        const int r = lane + 32 * i;
+        const bool on = w.it.q0 + r < x.Tq;
+        v[i].x = on ? __ldg(x.lse + row0 + (long long)r * x.H) * -kLog2e : -INFINITY;  // 2^(s c - inf) = 0: no weight
+        v[i].y = on ? -__ldg(x.delta + row0 + (long long)r * x.H) : 0.f;
       }
-      if (ok) mbar_arrive_warp(bar(B_STFULL));
+      if (w.i > 0 && !mbar_wait_warp(bar(B_STEMPTY), (w.i - 1) & 1, ctl)) break;
+#pragma unroll
+      for (int i = 0; i < BR / 32; ++i) stat[lane + 32 * i] = v[i];
+      mbar_arrive_warp(bar(B_STFULL));
     }
-  } else {
-    // ---- softmax
-    const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane;
+  } else if (warp >= 4) {
+    // ---- softmax: lane = query row, each of a quadrant's four warps a quarter of the columns
+    const int quad = warp & 3, part = (warp - 4) >> 2, row = quad * 32 + lane;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
-    const float c = x.scale * kLog2e;
+    const float2 c2 = make_float2(x.scale * kLog2e, x.scale * kLog2e);
     bool ok = true, pend = false;
     int n = 0, ni = 0;      // key tiles, items with any
     long long prow = 0;     // the pending output's row
     bool pvalid = false;
-    auto emit = [&]() -> bool {  // the pending item's dq, this half's columns
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ACC), (ni - 1) & 1, ctl))) return false;
+    auto emit = [&]() -> bool {  // the pending item's dq, this quarter's columns
+      if (!mbar_wait_warp(bar(B_ACC), (ni - 1) & 1, ctl)) return false;
       tc_fence_after();
-#pragma unroll 1
-      for (int q = half * (D / 64); q < (half + 1) * (D / 64); ++q) {
-        float v[32];
-        tmem_ld32(la + COL_Q + 32 * q, v);
+#pragma unroll
+      for (int q = part * (D / 64); q < (part + 1) * (D / 64); ++q) {
+        float v[16];
+        tmem_ld16(la + COL_Q + 16 * q, v);
         tmem_wait_ld();
-        if (pvalid) emit32(x.dq, x.part, prow * D + 32 * q, v, x.scale);
+        if (pvalid) emit16(x.dq, x.part, prow * D + 16 * q, v, x.scale);
       }
       tc_fence_before();
       return true;
@@ -440,61 +383,51 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
       const long long orow = ((long long)it.b * x.Tq + it.q0 + row) * x.H + it.h + (x.part != nullptr ? it.sp * rows : 0);
       if (it.nt == 0) {  // no states: dq is zero (a split without states leaves nothing)
         if (valid && x.part == nullptr) {
-          float z[32];
+          float z[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = 0.f;
-          for (int q = half * (D / 64); q < (half + 1) * (D / 64); ++q) emit32(x.dq, nullptr, orow * D + 32 * q, z, 1.f);
+          for (int i = 0; i < 16; ++i) z[i] = 0.f;
+          for (int q = part * (D / 64); q < (part + 1) * (D / 64); ++q) emit16(x.dq, nullptr, orow * D + 16 * q, z, 1.f);
         }
         continue;
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_STFULL), ni & 1, ctl))) { ok = false; break; }
+      if (!mbar_wait_warp(bar(B_STFULL), ni & 1, ctl)) { ok = false; break; }
       const float2 st = stat[row];
       mbar_arrive_warp(bar(B_STEMPTY));
+      const float2 nl2 = make_float2(st.x, st.x), nd2 = make_float2(st.y, st.y);
       for (int j = 0; j < it.nt; ++j, ++n) {
-        const uint32_t sb = la + COL_S + 128 * (n & 1) + 64 * half;
-        const int kv = it.nk - j * BR - 64 * half;  // valid columns of this half
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_SFULL + (n & 1)), (n >> 1) & 1, ctl))) { ok = false; break; }
+        const uint32_t sb = la + COL_S + 128 * (n & 1) + 32 * part;
+        const int kv = it.nk - j * BR - 32 * part;  // valid columns of this quarter
+        if (!mbar_wait_warp(bar(B_SFULL + (n & 1)), (n >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        float p[64];
-        tmem_ld32(sb, *reinterpret_cast<float(*)[32]>(p));
-        tmem_ld32(sb + 32, *reinterpret_cast<float(*)[32]>(p + 32));
+        float p[32];
+        tmem_ld32(sb, p);
         tmem_wait_ld();
-        const float2 c2 = make_float2(c, c), nl2 = make_float2(-st.x, -st.x), nd2 = make_float2(-st.y, -st.y);
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
+        for (int i = 0; i < 32; i += 2) {
           const float2 e = fma2(make_float2(p[i], p[i + 1]), c2, nl2);
           p[i] = ex2(e.x);
           p[i + 1] = ex2(e.y);
-        }
-        if (kv < 64) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) p[i] = i < kv ? p[i] : 0.f;
         }
         if (pend) {
           if (!emit()) { ok = false; break; }
           pend = false;
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_PFULL), n & 1, ctl))) { ok = false; break; }
+        if (!mbar_wait_warp(bar(B_PFULL), n & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        float pk[32];
-        {
-          float v[32];
+        float v[32];
+        tmem_ld32(la + COL_P + 32 * part, v);
+        tmem_wait_ld();
+        uint32_t pk[16];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            tmem_ld32(la + COL_P + 64 * half + 32 * q, v);
-            tmem_wait_ld();
-            if (kv < 64) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 32 * q + i < kv ? v[i] : 0.f;  // what V holds there may be NaN
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 d = mul2(make_float2(p[32 * q + 2 * i], p[32 * q + 2 * i + 1]), add2(make_float2(v[2 * i], v[2 * i + 1]), nd2));
-              pk[16 * q + i] = __uint_as_float(pack_bf16(d.x, d.y));
-            }
+        for (int i = 0; i < 16; ++i) {
+          float2 d = mul2(make_float2(p[2 * i], p[2 * i + 1]), add2(make_float2(v[2 * i], v[2 * i + 1]), nd2));
+          if (kv < 32) {  // selected, not multiplied: what V holds past the last state may be NaN
+            d.x = 2 * i < kv ? d.x : 0.f;
+            d.y = 2 * i + 1 < kv ? d.y : 0.f;
           }
+          pk[i] = pack_bf16(d.x, d.y);
         }
-        tmem_st32(sb, pk);  // over this half's own scores
+        tmem_st16(sb, pk);  // over this quarter's own scores
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive_warp(bar(B_DS));
@@ -733,33 +666,29 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
       mbar_arrive_warp(bar(B_STFULL + s));
     }
   } else if (warp >= 4) {
-    // ---- softmax: lane = state, columns = query rows
-    const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane;
+    // ---- softmax: lane = state, each of a quadrant's four warps a quarter of the columns (query rows)
+    const int quad = warp & 3, part = (warp - 4) >> 2, row = quad * 32 + lane;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
     const float2 c2 = make_float2(x.scale * kLog2e, x.scale * kLog2e);
     bool ok = true, pend = false, pin = false, plive = false;
     int n = 0, ni = 0;
     long long prow = 0;  // the pending output's row; pin: inside L; plive: inside kv_len
-    auto emit = [&](bool zero) -> bool {
-      if (!zero) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ACC), (ni - 1) & 1, ctl))) return false;
-        tc_fence_after();
-      }
-#pragma unroll 1
-      for (int q = half * (D / 64); q < (half + 1) * (D / 64); ++q) {
-        float v[32], u[32];
-        if (!zero) {
-          tmem_ld32(la + COL_V + 32 * q, v);
-          tmem_ld32(la + COL_K + 32 * q, u);
-          tmem_wait_ld();
-        }
-        if (zero || !plive) {
+    auto emit = [&]() -> bool {
+      if (!mbar_wait_warp(bar(B_ACC), (ni - 1) & 1, ctl)) return false;
+      tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = u[i] = 0.f;
+      for (int q = part * (D / 64); q < (part + 1) * (D / 64); ++q) {
+        float v[16], u[16];
+        tmem_ld16(la + COL_V + 16 * q, v);
+        tmem_ld16(la + COL_K + 16 * q, u);
+        tmem_wait_ld();
+        if (!plive) {  // selected: a row past the last state may hold NaN
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = u[i] = 0.f;
         }
         if (pin) {
-          emit32(x.dv, x.part2, prow * D + 32 * q, v, 1.f);
-          emit32(x.dk, x.part, prow * D + 32 * q, u, x.scale);
+          emit16(x.dv, x.part2, prow * D + 16 * q, v, 1.f);
+          emit16(x.dk, x.part, prow * D + 16 * q, u, x.scale);
         }
       }
       tc_fence_before();
@@ -769,35 +698,34 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
     ItemPos pos;
     for (pos.start(x.grid); ok && pos.on(x.grid); pos.next(x.grid)) {
       const KItem it = decode_k(x, pos);
-      const bool in = it.k0 + row < x.L, live = it.k0 + row < valid_states(x, it.b);
+      const bool in = it.k0 + row < x.L, live = it.k0 + row < valid_states_warp(x, it.b);
       const long long orow = ((long long)it.b * x.L + it.k0 + row) * x.Hkv + it.hk + (x.part != nullptr ? it.sp * rows : 0);
-      if (it.nt == 0) {  // past the last state (or no rows in this split, which leaves nothing): zeros
-        if (x.part == nullptr) {
-          const bool a = pin, bq = plive;
-          const long long r = prow;
-          pin = in;
-          prow = orow;
-          emit(true);
-          pin = a;
-          plive = bq;
-          prow = r;
+      if (it.nt == 0) {  // past the last state: zeros (which the join writes where there are partial sums)
+        if (in && x.part == nullptr) {
+          float z[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = 0.f;
+          for (int q = part * (D / 64); q < (part + 1) * (D / 64); ++q) {
+            emit16(x.dv, nullptr, orow * D + 16 * q, z, 1.f);
+            emit16(x.dk, nullptr, orow * D + 16 * q, z, 1.f);
+          }
         }
         continue;
       }
       for (int j = 0; j < it.nt; ++j, ++n) {
-        const float4* nl = reinterpret_cast<const float4*>(stat + 2 * (n & 1) * BR + 64 * half);
+        const float4* nl = reinterpret_cast<const float4*>(stat + 2 * (n & 1) * BR + 32 * part);
         const float4* nd = nl + BR / 4;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_STFULL + (n & 1)), (n >> 1) & 1, ctl) && mbar_wait(bar(B_SFULL), n & 1, ctl))) {
+        if (!mbar_wait_warp(bar(B_STFULL + (n & 1)), (n >> 1) & 1, ctl) || !mbar_wait_warp(bar(B_SFULL), n & 1, ctl)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        float p[64], pk[32];
-        tmem_ld32(la + COL_S + 64 * half, *reinterpret_cast<float(*)[32]>(p));
-        tmem_ld32(la + COL_S + 64 * half + 32, *reinterpret_cast<float(*)[32]>(p + 32));
+        float p[32];
+        uint32_t pk[16];
+        tmem_ld32(la + COL_S + 32 * part, p);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
+        for (int i = 0; i < 32; i += 4) {
           const float4 l = nl[i / 4];
           const float2 e = fma2(make_float2(p[i], p[i + 1]), c2, make_float2(l.x, l.y));
           const float2 f = fma2(make_float2(p[i + 2], p[i + 3]), c2, make_float2(l.z, l.w));
@@ -805,37 +733,31 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
           p[i + 1] = ex2(e.y);
           p[i + 2] = ex2(f.x);
           p[i + 3] = ex2(f.y);
-          pk[i / 2] = __uint_as_float(pack_bf16(p[i], p[i + 1]));
-          pk[i / 2 + 1] = __uint_as_float(pack_bf16(p[i + 2], p[i + 3]));
+          pk[i / 2] = pack_bf16(p[i], p[i + 1]);
+          pk[i / 2 + 1] = pack_bf16(p[i + 2], p[i + 3]);
         }
         if (pend) {
-          if (!emit(false)) { ok = false; break; }
+          if (!emit()) { ok = false; break; }
           pend = false;
         }
-        tmem_st32(la + COL_S + 64 * half, pk);
+        tmem_st16(la + COL_S + 32 * part, pk);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive_warp(bar(B_P));
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_PFULL), n & 1, ctl))) { ok = false; break; }
+        if (!mbar_wait_warp(bar(B_PFULL), n & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        {
-          float v[32];
+        float v[32];
+        tmem_ld32(la + COL_P + 32 * part, v);
+        tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            tmem_ld32(la + COL_P + 64 * half + 32 * q, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 d = nd[8 * q + i / 4];
-              const float2 e = mul2(make_float2(p[32 * q + i], p[32 * q + i + 1]), add2(make_float2(v[i], v[i + 1]), make_float2(d.x, d.y)));
-              const float2 f =
-                  mul2(make_float2(p[32 * q + i + 2], p[32 * q + i + 3]), add2(make_float2(v[i + 2], v[i + 3]), make_float2(d.z, d.w)));
-              pk[16 * q + i / 2] = __uint_as_float(pack_bf16(e.x, e.y));
-              pk[16 * q + i / 2 + 1] = __uint_as_float(pack_bf16(f.x, f.y));
-            }
-          }
+        for (int i = 0; i < 32; i += 4) {
+          const float4 d = nd[i / 4];
+          const float2 e = mul2(make_float2(p[i], p[i + 1]), add2(make_float2(v[i], v[i + 1]), make_float2(d.x, d.y)));
+          const float2 f = mul2(make_float2(p[i + 2], p[i + 3]), add2(make_float2(v[i + 2], v[i + 3]), make_float2(d.z, d.w)));
+          pk[i / 2] = pack_bf16(e.x, e.y);
+          pk[i / 2 + 1] = pack_bf16(f.x, f.y);
         }
-        tmem_st32(la + COL_P + 64 * half, pk);
+        tmem_st16(la + COL_P + 32 * part, pk);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive_warp(bar(B_DS));
@@ -848,12 +770,44 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
       prow = orow;
       ++ni;
     }
-    if (ok && pend) emit(false);
+    if (ok && pend) emit();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_free(tmem, 512);
+}
+
+// ----------------------------------------------------------------- Delta --
+// <dO, o> of every query row: 16 bytes a lane, D / 8 lanes a row, coalesced over rows that follow one another.
+// (Formed by two warps of the dq kernel instead, it held that kernel back: 1,171 against 1,040 us with both kernels at
+// 90,720 x 24 rows.)
+template <int D>
+__global__ void __launch_bounds__(256) k_xattn_delta_bf16(const XbDev x, long long rows) {
+  constexpr int LR = D / 8, U = 4;  // U rows a thread, loads first
+  const long long base = (long long)blockIdx.x * (256 / LR) * U + threadIdx.x / LR;
+  const int li = threadIdx.x % LR;
+  uint4 a[U], g[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = min(base + u * (256 / LR), rows - 1);
+    a[u] = __ldg(reinterpret_cast<const uint4*>(x.y + row * D) + li);
+    g[u] = __ldg(reinterpret_cast<const uint4*>(x.dy + row * D) + li);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t av[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, gv[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s = fmaf(__uint_as_float(av[i] << 16), __uint_as_float(gv[i] << 16), s);
+      s = fmaf(__uint_as_float(av[i] & 0xFFFF0000u), __uint_as_float(gv[i] & 0xFFFF0000u), s);
+    }
+#pragma unroll
+    for (int o = LR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const long long row = base + u * (256 / LR);
+    if (li == 0 && row < rows) x.delta[row] = s;
+  }
 }
 
 // --------------------------------------------------------- joining splits --
@@ -962,7 +916,9 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_xattn_dq_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smq);
   if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(k_xattn_dkv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smk)) != cudaSuccess) return e;
-  // dq first: it forms Delta
+  const long long rows = (long long)d.B * d.Tq * d.H, per = 256 / (D / 8) * 4;
+  k_xattn_delta_bf16<D><<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(x, rows);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   XbDev xq = x;
   xq.ns = c.qs;
   const int qgrid = (int)(qi < kSms ? qi : kSms), kgrid = (int)(ki < kSms ? ki : kSms);
