@@ -11,14 +11,16 @@
 //
 // Bound by HBM: 9 (16 backward) flops an element against 4 bytes or more.  A
 // row (one head of one token) is held by LPR lanes with 8 columns each, so
-// every access is a 16-byte vector and the row's sums are shuffles.  A block's
-// row slots are fixed to heads: the norm's weights, and in the backward their
-// gradient, stay in registers over all the tokens that the block walks, and a
-// token's table row is read by all of a block's heads at the same time (one
-// read from L2, the others from L1).  Each thread has several tokens' loads in
-// flight before it works on the first.
-// The weights' gradient: every block writes its sums (fp32), a second kernel
-// adds them in a fixed order, so results do not depend on timing.
+// every access is a 16-byte vector and the row's sums are shuffles.  A thread
+// has the same columns of HU heads of a token: the token's positions and its
+// angles are read and addressed once for all of them (with one head a thread
+// the instructions around the data, 25 an element, kept the kernel at 55 % of
+// the memory's rate).  Its heads stay the same over all the tokens that the
+// block walks, so the norm's weights, and in the backward their gradient, stay
+// in registers.  With few heads a thread has U tokens in flight instead.
+// The weights' gradient: a block adds its threads' sums in shared memory and
+// writes them (fp32), a second kernel adds the blocks', both in a fixed order,
+// so results do not depend on timing.
 #include <cuda_bf16.h>
 
 #include "vdn_internal.h"
@@ -35,12 +37,12 @@ struct QkDev {
   const int* pos;
   void *qo, *ko;          // forward: outputs; backward: dq, dk (dense)
   const void *gq, *gk;    // backward: gradients of the outputs (dense)
-  float* part;            // backward: [rows][Hq + Hk][d] partial weight gradients, or null
+  float* part;            // backward: partial weight gradients [gx][Hq + Hk][d], or [gx nch][2][d] for shared weights; or null
   long long tokens;
   int Hq, Ht, d, rot, axes, rows;  // rows: table rows
   int sec0, sec01;                 // first pair of axis 1 and of axis 2
   int per_head, vec;               // vec: no lane's pairs straddle two axes
-  int hc, tpi, nch, gx;            // heads per chunk, tokens per block step, chunks, blocks per chunk
+  int hc, tpi, nch, gx;            // head slots of a block, tokens per block step, head chunks (of HU hc heads), blocks per chunk
   float eps;
 };
 
@@ -180,169 +182,199 @@ __device__ __forceinline__ bool positions(const QkDev& a, long long t, int (&p)[
   return ok;
 }
 
-// Where this thread's row slot lies: lane within the row, token of the step, head.
-template <int LPR>
+// Where this thread's row slot lies: lane within the row, token of the step, its heads.
+template <int LPR, int HU>
 struct Slot {
-  int li, ti, head;
+  int li, ti, head0;  // head i of the thread: head0 + i hc
   bool active;
   __device__ __forceinline__ Slot(const QkDev& a) {
     const int lane = threadIdx.x & 31, slot = threadIdx.x / LPR;
     li = lane % LPR;
     ti = slot / a.hc;
-    head = (int)(blockIdx.x % a.nch) * a.hc + slot % a.hc;
-    active = ti < a.tpi && head < a.Ht && 8 * li < a.d;
+    head0 = (int)(blockIdx.x % a.nch) * a.hc * HU + slot % a.hc;
+    active = ti < a.tpi && 8 * li < a.d;
   }
 };
 
-template <int LPR>
-__device__ __forceinline__ void load_weight(const QkDev& a, const Slot<LPR>& s, float (&w)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 1.f;
-  if (!s.active) return;
-  const bool isq = s.head < a.Hq;
-  const float* p = isq ? a.wq : a.wk;
-  if (p == nullptr) return;
-  p += (a.per_head ? (long long)(isq ? s.head : s.head - a.Hq) * a.d : 0) + 8 * s.li;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = __ldg(p + i);
-}
-
-template <typename T, int LPR, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 4) k_qk_fwd(const QkDev a) {
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // tokens in flight per thread
-  const Slot<LPR> s(a);
+// One head of a thread: where its columns lie in the inputs and outputs, and the norm's weights there.
+template <typename T>
+struct Head {
+  const T* x;
+  T* o;
+  long long off, xs, os;  // offset within a token of a dense [tokens, H, d] tensor, token strides of input and output
   float w[8];
-  load_weight(a, s, w);
+  bool on, isq;
+  __device__ __forceinline__ void init(const QkDev& a, int head, int li, bool active) {
+    on = active && head < a.Ht;
+    isq = head < a.Hq;
+    const int h = isq ? head : head - a.Hq;
+    off = (long long)h * a.d + 8 * li;
+    xs = isq ? a.qs : a.ks;
+    os = (long long)(isq ? a.Hq : a.Ht - a.Hq) * a.d;
+    x = static_cast<const T*>(isq ? a.q : a.k) + off;
+    o = static_cast<T*>(isq ? a.qo : a.ko) + off;
+    const float* p = isq ? a.wq : a.wk;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = on && p != nullptr ? __ldg(p + (a.per_head ? off : 8 * li) + i) : 1.f;
+  }
+};
+
+template <typename T, int LPR, bool SPLIT, int HU, int U>
+__global__ void __launch_bounds__(kThreads, 3) k_qk_fwd(const QkDev a) {
+  const Slot<LPR, HU> s(a);
+  Head<T> hd[HU];
+#pragma unroll
+  for (int i = 0; i < HU; ++i) hd[i].init(a, s.head0 + i * a.hc, s.li, s.active);
   Turn<LPR, SPLIT> turn(a, s.li, threadIdx.x & 31);
-  const bool isq = s.head < a.Hq;
-  const int h = isq ? s.head : s.head - a.Hq, Hx = isq ? a.Hq : a.Ht - a.Hq;
-  const long long xs = isq ? a.qs : a.ks, off = (long long)h * a.d + 8 * s.li;
-  const T* x0 = static_cast<const T*>(isq ? a.q : a.k) + off;
-  T* o0 = static_cast<T*>(isq ? a.qo : a.ko) + off;
-  const long long os = (long long)Hx * a.d, step = (long long)a.gx * a.tpi;
+  const long long step = (long long)a.gx * a.tpi;
   const float inv_d = 1.0f / (float)a.d;
   for (long long base = (long long)(blockIdx.x / a.nch) * a.tpi; base < a.tokens; base += U * step) {
-    Raw<T> raw[U];
+    Raw<T> raw[U][HU];
     int p[U][3];
     bool on[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const long long t = base + u * step + s.ti;
       on[u] = s.active && t < a.tokens;
-      raw[u] = on[u] ? load_raw(x0 + t * xs) : zero_raw<T>();
+#pragma unroll
+      for (int i = 0; i < HU; ++i) raw[u][i] = on[u] && hd[i].on ? load_raw(hd[i].x + t * hd[i].xs) : zero_raw<T>();
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) on[u] = on[u] && positions(a, base + u * step + s.ti, p[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const long long t = base + u * step + s.ti;
-      on[u] = on[u] && positions(a, t, p[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[8], ss = 0.f;
-      expand(raw[u], x);
       if (on[u]) turn.angles(a, p[u]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, a.eps));
+      for (int i = 0; i < HU; ++i) {
+        float x[8], ss = 0.f;
+        expand(raw[u][i], x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= rstd * w[i];
-      turn.apply(x, 1.f);
-      if (on[u]) store8(o0 + (base + u * step + s.ti) * os, x);
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+        const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, a.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= rstd * hd[i].w[e];
+        turn.apply(x, 1.f);
+        if (on[u] && hd[i].on) store8(hd[i].o + t * hd[i].os, x);
+      }
     }
   }
 }
 
-template <typename T, typename G, int LPR, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 4) k_qk_bwd(const QkDev a) {
-  constexpr int U = sizeof(T) == 2 ? 2 : 1;
-  const Slot<LPR> s(a);
-  float w[8], acc[8];
-  load_weight(a, s, w);
+template <typename T, typename G, int LPR, bool SPLIT, int HU, int U>
+__global__ void __launch_bounds__(kThreads, 2) k_qk_bwd(const QkDev a) {
+  const Slot<LPR, HU> s(a);
+  Head<T> hd[HU];
+  float acc[HU][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int i = 0; i < HU; ++i) {
+    hd[i].init(a, s.head0 + i * a.hc, s.li, s.active);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
+  }
   Turn<LPR, SPLIT> turn(a, s.li, threadIdx.x & 31);
-  const bool isq = s.head < a.Hq;
-  const int h = isq ? s.head : s.head - a.Hq, Hx = isq ? a.Hq : a.Ht - a.Hq;
-  const long long xs = isq ? a.qs : a.ks, off = (long long)h * a.d + 8 * s.li;
-  const T* x0 = static_cast<const T*>(isq ? a.q : a.k) + off;
-  const G* g0 = static_cast<const G*>(isq ? a.gq : a.gk) + off;
-  T* o0 = static_cast<T*>(isq ? a.qo : a.ko) + off;
-  const long long os = (long long)Hx * a.d, step = (long long)a.gx * a.tpi;
+  const long long step = (long long)a.gx * a.tpi;
   const float inv_d = 1.0f / (float)a.d;
   for (long long base = (long long)(blockIdx.x / a.nch) * a.tpi; base < a.tokens; base += U * step) {
-    Raw<T> rx[U];
-    Raw<G> rg[U];
+    Raw<T> rx[U][HU];
+    Raw<G> rg[U][HU];
     int p[U][3];
     bool on[U], in[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const long long t = base + u * step + s.ti;
       in[u] = s.active && t < a.tokens;
-      rx[u] = in[u] ? load_raw(x0 + t * xs) : zero_raw<T>();
-      rg[u] = in[u] ? load_raw(g0 + t * os) : zero_raw<G>();
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      on[u] = in[u] && positions(a, base + u * step + s.ti, p[u]);
-      // a skipped token's output does not depend on its input: its gradient is
-      // zero, whatever the two arrays hold there
-      if (in[u] && !on[u]) {
-        rx[u] = zero_raw<T>();
-        rg[u] = zero_raw<G>();
+      for (int i = 0; i < HU; ++i) {
+        const bool ld = in[u] && hd[i].on;
+        rx[u][i] = ld ? load_raw(hd[i].x + t * hd[i].xs) : zero_raw<T>();
+        rg[u][i] = ld ? load_raw(static_cast<const G*>(hd[i].isq ? a.gq : a.gk) + hd[i].off + t * hd[i].os) : zero_raw<G>();
       }
     }
 #pragma unroll
+    for (int u = 0; u < U; ++u) on[u] = in[u] && positions(a, base + u * step + s.ti, p[u]);
+#pragma unroll
     for (int u = 0; u < U; ++u) {
-      float x[8], g[8], ss = 0.f, dot = 0.f;
-      expand(rx[u], x);
-      expand(rg[u], g);
+      const long long t = base + u * step + s.ti;
       if (on[u]) turn.angles(a, p[u]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      turn.apply(g, -1.f);
-      const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, a.eps));
+      for (int i = 0; i < HU; ++i) {
+        float x[8], g[8], ss = 0.f, dot = 0.f;
+        expand(rx[u][i], x);
+        expand(rg[u][i], g);
+        if (!on[u]) {
+          // a skipped token's output does not depend on its input: its gradient is zero, whatever the two arrays hold there
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] *= rstd;
-        acc[i] = fmaf(g[i], x[i], acc[i]);
-        g[i] *= w[i];
-        dot = fmaf(g[i], x[i], dot);
+          for (int e = 0; e < 8; ++e) x[e] = g[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+        turn.apply(g, -1.f);
+        const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, a.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] *= rstd;
+          acc[i][e] = fmaf(g[e], x[e], acc[i][e]);
+          g[e] *= hd[i].w[e];
+          dot = fmaf(g[e], x[e], dot);
+        }
+        dot = row_sum<LPR>(dot) * inv_d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = rstd * fmaf(-x[e], dot, g[e]);
+        if (in[u] && hd[i].on) store8(hd[i].o + t * hd[i].os, g);
       }
-      dot = row_sum<LPR>(dot) * inv_d;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = rstd * fmaf(-x[i], dot, g[i]);
-      if (in[u]) store8(o0 + (base + u * step + s.ti) * os, g);
     }
   }
-  if (a.part != nullptr && s.active) {
-    const long long row = (long long)(blockIdx.x / a.nch) * a.tpi + s.ti;
-    store8(a.part + (row * a.Ht + s.head) * a.d + 8 * s.li, acc);
+  if (a.part == nullptr) return;
+  // the block's sums: columns c of the LPR lanes' 8 LPR, slot after slot
+  __shared__ float buf[kThreads * 8];
+  constexpr int W = 8 * LPR, SLOTS = kThreads / LPR;
+  const int blk = blockIdx.x / a.nch, chunk = blockIdx.x % a.nch;
+  float sum[2] = {0.f, 0.f};  // shared weights: queries, keys
+#pragma unroll
+  for (int i = 0; i < HU; ++i) {
+    __syncthreads();
+    store8(buf + threadIdx.x * 8, acc[i]);
+    __syncthreads();
+    if (a.per_head) {
+      for (int j = threadIdx.x; j < a.hc * W; j += kThreads) {
+        const int hs = j / W, c = j % W, head = chunk * a.hc * HU + hs + i * a.hc;
+        float v = 0.f;
+        for (int t = 0; t < a.tpi; ++t) v += buf[(t * a.hc + hs) * W + c];
+        if (head < a.Ht && c < a.d) a.part[((long long)blk * a.Ht + head) * a.d + c] = v;
+      }
+    } else if (threadIdx.x < W) {
+      for (int sl = 0; sl < SLOTS && sl < a.hc * a.tpi; ++sl) {
+        const int head = chunk * a.hc * HU + sl % a.hc + i * a.hc;
+        if (head < a.Ht) sum[head < a.Hq ? 0 : 1] += buf[sl * W + threadIdx.x];
+      }
+    }
+  }
+  if (!a.per_head && threadIdx.x < W && threadIdx.x < a.d) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) a.part[(((long long)blk * a.nch + chunk) * 2 + k) * a.d + threadIdx.x] = sum[k];
   }
 }
 
-// dw[j] = sum of the partials.  A block has 32 columns and 32 row lanes; per
-// head one block column per head, else a head set is summed together.
+// dw[j] = sum of the blocks' partials, rows of `sets` [d].  A block has 32
+// columns and 32 row lanes; one block column for each set (a head, or 0 =
+// queries and 1 = keys).
 __global__ void __launch_bounds__(1024) k_qk_dw(const float* __restrict__ part, float* __restrict__ dwq,
-                                                float* __restrict__ dwk, int rows, int Hq, int Ht, int d, int per_head) {
+                                                float* __restrict__ dwk, int rows, int sets, int nq, int d) {
   __shared__ float red[32][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), rl = threadIdx.x >> 5;
-  const int set = blockIdx.y;  // a head, or 0 = queries and 1 = keys
-  const int h0 = per_head ? set : (set == 0 ? 0 : Hq), h1 = per_head ? set + 1 : (set == 0 ? Hq : Ht);
-  const bool isq = h0 < Hq;
-  float* dst = isq ? dwq : dwk;
-  if (dst == nullptr || h0 >= h1) return;  // uniform over the block
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), rl = threadIdx.x >> 5, set = blockIdx.y;
+  float* dst = set < nq ? dwq : dwk;
+  if (dst == nullptr) return;  // uniform over the block
   float s = 0.f;
-  if (c < d) {
-    const int nh = h1 - h0, n = rows * nh;
-    for (int i = rl; i < n; i += 32) s += part[((long long)(i / nh) * Ht + h0 + i % nh) * d + c];
-  }
+  if (c < d)
+    for (int i = rl; i < rows; i += 32) s += part[((long long)i * sets + set) * d + c];
   red[rl][threadIdx.x & 31] = s;
   __syncthreads();
   if (rl == 0 && c < d) {
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v += red[i][threadIdx.x & 31];
-    dst[per_head ? (long long)(isq ? h0 : h0 - Hq) * d + c : c] = v;
+    dst[(long long)(set < nq ? set : set - nq) * d + c] = v;
   }
 }
 
@@ -355,24 +387,34 @@ int lanes_per_row(int d) {
   return l < 2 ? 2 : l;
 }
 
+// Heads of a thread: several where a block's row slots still hold all the heads
+// of a token or nearly so (at most an eighth of the threads' heads unused).
+int heads_per_thread(const vdn_qk_cfg& c, bool f32) {
+  const int lpr = lanes_per_row(c.d), slots = kThreads / lpr, ht = c.Hq + c.Hk, hu = f32 ? 2 : 3;
+  if (lpr < 8) return 1;
+  const int nch = (ht + slots * hu - 1) / (slots * hu), hc = (ht + nch * hu - 1) / (nch * hu);
+  const int used = slots / hc * hc;  // row slots with a token
+  return 8 * (long long)ht * used >= 7LL * nch * hc * hu * slots ? hu : 1;
+}
+
 // Row slots of a block: chunks of heads of equal size, and as many tokens per
 // step as fit beside one chunk.
-void qk_slots(const vdn_qk_cfg& c, int* hc, int* tpi, int* nch) {
+void qk_slots(const vdn_qk_cfg& c, int hu, int* hc, int* tpi, int* nch) {
   const int slots = kThreads / lanes_per_row(c.d), ht = c.Hq + c.Hk;
-  *nch = (ht + slots - 1) / slots;
-  *hc = (ht + *nch - 1) / *nch;
+  *nch = (ht + slots * hu - 1) / (slots * hu);
+  *hc = (ht + *nch * hu - 1) / (*nch * hu);
   *tpi = slots / *hc;
 }
 
-// The block's row slots over heads and tokens, and the grid: four blocks on
-// every SM, or fewer when there are fewer tokens.
-bool plan(const vdn_qk_cfg& c, QkDev& a) {
+// The block's row slots over heads and tokens, and the grid: `resident` blocks
+// on every SM, or fewer when there are fewer tokens.
+bool plan(const vdn_qk_cfg& c, QkDev& a, int hu, int resident) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return false;
-  qk_slots(c, &a.hc, &a.tpi, &a.nch);
+  qk_slots(c, hu, &a.hc, &a.tpi, &a.nch);
   const long long steps = (c.tokens + a.tpi - 1) / a.tpi;
-  long long gx = (long long)4 * sms / a.nch;
+  long long gx = (long long)resident * sms / a.nch;
   if (gx > qk_max_blocks(a.nch)) gx = qk_max_blocks(a.nch);
   if (gx < 1) gx = 1;
   a.gx = (int)(steps < gx ? steps : gx);
@@ -398,33 +440,45 @@ QkDev device_args(const vdn_qk_cfg& c, const vdn_qk_args& in) {
 }
 
 template <typename T, int LPR>
-void run_fwd(const QkDev& a, bool split, unsigned grid, cudaStream_t s) {
-  if (split) k_qk_fwd<T, LPR, true><<<grid, kThreads, 0, s>>>(a);
-  else k_qk_fwd<T, LPR, false><<<grid, kThreads, 0, s>>>(a);
+void run_fwd(const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
+  constexpr int HU = LPR < 8 ? 1 : sizeof(T) == 2 ? 3 : 2, U = sizeof(T) == 2 ? 4 : 2;
+  if (hu > 1) {
+    if (split) k_qk_fwd<T, LPR, true, HU, 1><<<grid, kThreads, 0, s>>>(a);
+    else k_qk_fwd<T, LPR, false, HU, 1><<<grid, kThreads, 0, s>>>(a);
+  } else {
+    if (split) k_qk_fwd<T, LPR, true, 1, U><<<grid, kThreads, 0, s>>>(a);
+    else k_qk_fwd<T, LPR, false, 1, U><<<grid, kThreads, 0, s>>>(a);
+  }
 }
 template <typename T, typename G, int LPR>
-void run_bwd(const QkDev& a, bool split, unsigned grid, cudaStream_t s) {
-  if (split) k_qk_bwd<T, G, LPR, true><<<grid, kThreads, 0, s>>>(a);
-  else k_qk_bwd<T, G, LPR, false><<<grid, kThreads, 0, s>>>(a);
+void run_bwd(const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
+  constexpr int HU = LPR < 8 ? 1 : sizeof(T) == 2 ? 3 : 2, U = sizeof(T) == 2 ? 3 : 2;
+  if (hu > 1) {
+    if (split) k_qk_bwd<T, G, LPR, true, HU, 1><<<grid, kThreads, 0, s>>>(a);
+    else k_qk_bwd<T, G, LPR, false, HU, 1><<<grid, kThreads, 0, s>>>(a);
+  } else {
+    if (split) k_qk_bwd<T, G, LPR, true, 1, U><<<grid, kThreads, 0, s>>>(a);
+    else k_qk_bwd<T, G, LPR, false, 1, U><<<grid, kThreads, 0, s>>>(a);
+  }
 }
 template <typename T>
-void fwd_lanes(int lpr, const QkDev& a, bool split, unsigned grid, cudaStream_t s) {
+void fwd_lanes(int lpr, const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
   switch (lpr) {
-    case 2: return run_fwd<T, 2>(a, split, grid, s);
-    case 4: return run_fwd<T, 4>(a, split, grid, s);
-    case 8: return run_fwd<T, 8>(a, split, grid, s);
-    case 16: return run_fwd<T, 16>(a, split, grid, s);
-    default: return run_fwd<T, 32>(a, split, grid, s);
+    case 2: return run_fwd<T, 2>(a, split, hu, grid, s);
+    case 4: return run_fwd<T, 4>(a, split, hu, grid, s);
+    case 8: return run_fwd<T, 8>(a, split, hu, grid, s);
+    case 16: return run_fwd<T, 16>(a, split, hu, grid, s);
+    default: return run_fwd<T, 32>(a, split, hu, grid, s);
   }
 }
 template <typename T, typename G>
-void bwd_lanes(int lpr, const QkDev& a, bool split, unsigned grid, cudaStream_t s) {
+void bwd_lanes(int lpr, const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
   switch (lpr) {
-    case 2: return run_bwd<T, G, 2>(a, split, grid, s);
-    case 4: return run_bwd<T, G, 4>(a, split, grid, s);
-    case 8: return run_bwd<T, G, 8>(a, split, grid, s);
-    case 16: return run_bwd<T, G, 16>(a, split, grid, s);
-    default: return run_bwd<T, G, 32>(a, split, grid, s);
+    case 2: return run_bwd<T, G, 2>(a, split, hu, grid, s);
+    case 4: return run_bwd<T, G, 4>(a, split, hu, grid, s);
+    case 8: return run_bwd<T, G, 8>(a, split, hu, grid, s);
+    case 16: return run_bwd<T, G, 16>(a, split, hu, grid, s);
+    default: return run_bwd<T, G, 32>(a, split, hu, grid, s);
   }
 }
 
@@ -432,36 +486,39 @@ void bwd_lanes(int lpr, const QkDev& a, bool split, unsigned grid, cudaStream_t 
 
 size_t qk_bwd_workspace(const vdn_qk_cfg& c) {
   int hc, tpi, nch;
-  qk_slots(c, &hc, &tpi, &nch);
-  return (size_t)qk_max_blocks(nch) * tpi * (c.Hq + c.Hk) * c.d * sizeof(float);
+  qk_slots(c, heads_per_thread(c, c.dtype == VDN_F32), &hc, &tpi, &nch);
+  return (size_t)qk_max_blocks(nch) * (c.per_head ? c.Hq + c.Hk : 2 * nch) * c.d * sizeof(float);
 }
 
 cudaError_t launch_qk_fwd(const vdn_qk_cfg& c, const vdn_qk_args& in, cudaStream_t s) {
   QkDev a = device_args(c, in);
-  if (!plan(c, a)) return cudaErrorInvalidDevice;
+  const int hu = heads_per_thread(c, c.dtype == VDN_F32);
+  if (!plan(c, a, hu, 3)) return cudaErrorInvalidDevice;
   const unsigned grid = (unsigned)a.gx * a.nch;
   const bool split = c.pairing == VDN_PAIR_SPLIT;
-  if (c.dtype == VDN_BF16) fwd_lanes<__nv_bfloat16>(lanes_per_row(c.d), a, split, grid, s);
-  else fwd_lanes<float>(lanes_per_row(c.d), a, split, grid, s);
+  if (c.dtype == VDN_BF16) fwd_lanes<__nv_bfloat16>(lanes_per_row(c.d), a, split, hu, grid, s);
+  else fwd_lanes<float>(lanes_per_row(c.d), a, split, hu, grid, s);
   return cudaGetLastError();
 }
 
 cudaError_t launch_qk_bwd(const vdn_qk_cfg& c, const vdn_qk_args& in, const vdn_qk_grads& g, cudaStream_t s) {
   QkDev a = device_args(c, in);
-  if (!plan(c, a)) return cudaErrorInvalidDevice;
+  const int hu = heads_per_thread(c, c.dtype == VDN_F32);
+  if (!plan(c, a, hu, 2)) return cudaErrorInvalidDevice;
   a.qo = g.dq; a.ko = g.dk; a.gq = g.dq_out; a.gk = g.dk_out;
   const bool want = g.dwq != nullptr || g.dwk != nullptr;
   a.part = want ? static_cast<float*>(g.workspace) : nullptr;
   const unsigned grid = (unsigned)a.gx * a.nch;
   const bool split = c.pairing == VDN_PAIR_SPLIT;
   const int lpr = lanes_per_row(c.d);
-  if (c.dtype == VDN_F32) bwd_lanes<float, float>(lpr, a, split, grid, s);
-  else if (c.grad_dtype == VDN_F32) bwd_lanes<__nv_bfloat16, float>(lpr, a, split, grid, s);
-  else bwd_lanes<__nv_bfloat16, __nv_bfloat16>(lpr, a, split, grid, s);
+  if (c.dtype == VDN_F32) bwd_lanes<float, float>(lpr, a, split, hu, grid, s);
+  else if (c.grad_dtype == VDN_F32) bwd_lanes<__nv_bfloat16, float>(lpr, a, split, hu, grid, s);
+  else bwd_lanes<__nv_bfloat16, __nv_bfloat16>(lpr, a, split, hu, grid, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !want) return e;
-  k_qk_dw<<<dim3((c.d + 31) / 32, c.per_head ? a.Ht : 2), 1024, 0, s>>>(a.part, g.dwq, g.dwk, a.gx * a.tpi, c.Hq, a.Ht,
-                                                                        c.d, c.per_head);
+  const int sets = c.per_head ? a.Ht : 2;
+  k_qk_dw<<<dim3((c.d + 31) / 32, sets), 1024, 0, s>>>(a.part, g.dwq, c.Hk > 0 ? g.dwk : nullptr, c.per_head ? a.gx : a.gx * a.nch,
+                                                       sets, c.per_head ? c.Hq : 1, c.d);
   return cudaGetLastError();
 }
 
