@@ -17,7 +17,10 @@
 // the instructions around the data, 25 an element, kept the kernel at 55 % of
 // the memory's rate).  Its heads stay the same over all the tokens that the
 // block walks, so the norm's weights, and in the backward their gradient, stay
-// in registers.  With few heads a thread has U tokens in flight instead.
+// in registers.  The tokens to come are copied into shared memory ahead
+// (cp.async; a row is copied and read by lanes of one warp, so no block barrier),
+// and the next token's angles into registers: with loads at their use the
+// threads waited for memory, and for the angles, between tokens.
 // The weights' gradient: a block adds its threads' sums in shared memory and
 // writes them (fp32), a second kernel adds the blocks', both in a fixed order,
 // so results do not depend on timing.
@@ -43,25 +46,60 @@ struct QkDev {
   int sec0, sec01;                 // first pair of axis 1 and of axis 2
   int per_head, vec;               // vec: no lane's pairs straddle two axes
   int hc, tpi, nch, gx;            // head slots of a block, tokens per block step, head chunks (of HU hc heads), blocks per chunk
+  int threads;                     // of a block: its row slots' lanes
   float eps;
 };
 
 // 8 consecutive elements as stored: one 16-byte vector (bf16) or two (fp32)
 template <typename T> struct Raw { uint4 v[sizeof(T) / 2]; };
 
-template <typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p) {
-  Raw<T> r;
+// The ring of a block: NV vectors of every thread for each of NS tokens.  A row's
+// 16-byte chunks lie in order; lane li copies chunks li, LPR + li (whole sectors
+// in every instruction) and reads the ones of its 8 columns.
+template <int NV, int NS, int LPR>
+struct Ring {
+  uint4* base;
+  int st;  // stage of the token at hand
+  __device__ __forceinline__ Ring(uint4* smem) : base(smem), st(0) {}
+  // vectors v .. v + V - 1 of the row of this thread's slot
+  template <int V>
+  __device__ __forceinline__ uint4* row(int stage, int v) const {
+    return base + (stage * NV + v) * kThreads + threadIdx.x / LPR * (LPR * V);
+  }
+  // the row at p (d elements, null: zeros) into vectors v.. of the stage `ahead` tokens on
+  template <typename T>
+  __device__ __forceinline__ void copy(int ahead, int v, const T* p, const void* any, int d) const {
+    constexpr int V = sizeof(T) / 2;
+    const int s = st + ahead >= NS ? st + ahead - NS : st + ahead, li = threadIdx.x % LPR;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-  return r;
-}
-template <typename T> __device__ __forceinline__ Raw<T> zero_raw() {
-  Raw<T> r;
+    for (int i = 0; i < V; ++i) {
+      const int c = i * LPR + li;
+      const bool on = p != nullptr && c * (16 / (int)sizeof(T)) < d;
+      const void* src = on ? static_cast<const void*>(reinterpret_cast<const uint4*>(p) + c) : any;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(row<V>(s, v) + c)),
+                   "l"(src), "r"(on ? 16 : 0)
+                   : "memory");
+    }
+  }
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // the token at hand has landed, for the whole warp
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+    __syncwarp();
+  }
+  template <typename T>
+  __device__ __forceinline__ Raw<T> read(int v) const {
+    constexpr int V = sizeof(T) / 2;
+    Raw<T> r;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = make_uint4(0, 0, 0, 0);
-  return r;
-}
+    for (int i = 0; i < V; ++i) r.v[i] = row<V>(st, v)[threadIdx.x % LPR * V + i];
+    return r;
+  }
+  __device__ __forceinline__ void next() {
+    __syncwarp();  // read by every lane, before any copies over it
+    st = st + 1 == NS ? 0 : st + 1;
+  }
+};
 __device__ __forceinline__ void expand(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
   const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
@@ -106,7 +144,8 @@ template <int LPR, bool SPLIT>
 struct Turn {
   int pair0, partner;  // first pair of this lane, lane holding the other half (SPLIT)
   bool on, second;     // this lane's columns are rotated; it holds the second half (SPLIT)
-  float cs[SPLIT ? 8 : 4], sn[SPLIT ? 8 : 4];
+  static constexpr int NP = SPLIT ? 8 : 4;
+  float cs[NP], sn[NP];
 
   __device__ __forceinline__ Turn(const QkDev& a, int li, int lane) {
     const int c = 8 * li, half = a.rot >> 1;
@@ -115,16 +154,22 @@ struct Turn {
     pair0 = SPLIT ? (second ? c - half : c) : (c >> 1);
     partner = !SPLIT || !on ? lane : (second ? lane - half / 8 : lane + half / 8);
 #pragma unroll
-    for (int i = 0; i < (SPLIT ? 8 : 4); ++i) {
+    for (int i = 0; i < NP; ++i) {
       cs[i] = 1.f;
       sn[i] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void take(const Turn& o) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      cs[i] = o.cs[i];
+      sn[i] = o.sn[i];
     }
   }
   // the angles of one token (its positions are inside the table)
   __device__ __forceinline__ void angles(const QkDev& a, const int (&p)[3]) {
     if (!on) return;
     const int half = a.rot >> 1;
-    constexpr int NP = SPLIT ? 8 : 4;
     if (a.vec) {
       const int r = pair0 >= a.sec01 ? p[2] : pair0 >= a.sec0 ? p[1] : p[0];
       const float4* t = reinterpret_cast<const float4*>(a.table + ((long long)r * half + pair0) * 2);
@@ -186,85 +231,117 @@ __device__ __forceinline__ bool positions(const QkDev& a, long long t, int (&p)[
 template <int LPR, int HU>
 struct Slot {
   int li, ti, head0;  // head i of the thread: head0 + i hc
-  bool active;
+  bool row, active;  // the slot has a token; the lane has columns
   __device__ __forceinline__ Slot(const QkDev& a) {
     const int lane = threadIdx.x & 31, slot = threadIdx.x / LPR;
     li = lane % LPR;
     ti = slot / a.hc;
     head0 = (int)(blockIdx.x % a.nch) * a.hc * HU + slot % a.hc;
-    active = ti < a.tpi && 8 * li < a.d;
+    row = ti < a.tpi;
+    active = row && 8 * li < a.d;
   }
 };
 
-// One head of a thread: where its columns lie in the inputs and outputs, and the norm's weights there.
-template <typename T>
+// One head of a thread: its columns' offset within a dense token, and the norm's weights there.
 struct Head {
-  const T* x;
-  T* o;
-  long long off, xs, os;  // offset within a token of a dense [tokens, H, d] tensor, token strides of input and output
-  float w[8];
+  int row, off;  // of the head; of the lane's columns
   bool on, isq;
+  float w[8];
   __device__ __forceinline__ void init(const QkDev& a, int head, int li, bool active) {
     on = active && head < a.Ht;
     isq = head < a.Hq;
-    const int h = isq ? head : head - a.Hq;
-    off = (long long)h * a.d + 8 * li;
-    xs = isq ? a.qs : a.ks;
-    os = (long long)(isq ? a.Hq : a.Ht - a.Hq) * a.d;
-    x = static_cast<const T*>(isq ? a.q : a.k) + off;
-    o = static_cast<T*>(isq ? a.qo : a.ko) + off;
+    row = head < a.Ht ? (isq ? head : head - a.Hq) * a.d : -1;
+    off = (isq ? head : head - a.Hq) * a.d + 8 * li;
     const float* p = isq ? a.wq : a.wk;
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = on && p != nullptr ? __ldg(p + (a.per_head ? off : 8 * li) + i) : 1.f;
   }
+  // the columns in a pair of tensors, the token tq (tk) elements from their start
+  template <typename P>
+  __device__ __forceinline__ P* at(P* q, P* k, long long tq, long long tk) const {
+    return (isq ? q + tq : k + tk) + off;
+  }
+  // the head's row there
+  template <typename P>
+  __device__ __forceinline__ P* row_at(P* q, P* k, long long tq, long long tk) const {
+    return (isq ? q + tq : k + tk) + row;
+  }
 };
 
-template <typename T, int LPR, bool SPLIT, int HU, int U>
+template <typename T, int HU> constexpr int fwd_stages() { return HU > 1 ? 4 : sizeof(T) == 2 ? 8 : 4; }
+template <typename T, int HU> constexpr size_t fwd_smem() {
+  return (size_t)fwd_stages<T, HU>() * HU * (sizeof(T) / 2) * kThreads * 16;
+}
+template <typename T, typename G, int HU> constexpr int bwd_vectors() { return HU * (int)(sizeof(T) + sizeof(G)) / 2; }
+template <typename T, typename G, int HU> constexpr int bwd_stages() { return bwd_vectors<T, G, HU>() >= 8 ? 3 : 4; }
+template <typename T, typename G, int HU> constexpr size_t bwd_smem() {
+  return (size_t)bwd_stages<T, G, HU>() * bwd_vectors<T, G, HU>() * kThreads * 16;
+}
+
+template <typename T, int LPR, bool SPLIT, int HU>
 __global__ void __launch_bounds__(kThreads, 3) k_qk_fwd(const QkDev a) {
+  constexpr int NS = fwd_stages<T, HU>(), V = sizeof(T) / 2;
+  extern __shared__ uint4 qk_smem[];
+  Ring<HU * V, NS, LPR> ring(qk_smem);
   const Slot<LPR, HU> s(a);
-  Head<T> hd[HU];
+  Head hd[HU];
 #pragma unroll
   for (int i = 0; i < HU; ++i) hd[i].init(a, s.head0 + i * a.hc, s.li, s.active);
   Turn<LPR, SPLIT> turn(a, s.li, threadIdx.x & 31);
-  const long long step = (long long)a.gx * a.tpi;
+  const long long step = (long long)a.gx * a.tpi, dq = (long long)a.Hq * a.d, dk = (long long)(a.Ht - a.Hq) * a.d;
   const float inv_d = 1.0f / (float)a.d;
-  for (long long base = (long long)(blockIdx.x / a.nch) * a.tpi; base < a.tokens; base += U * step) {
-    Raw<T> raw[U][HU];
-    int p[U][3];
-    bool on[U];
+  auto fetch = [&](int ahead, long long t) {
+    const bool on = s.row && t < a.tokens;
+    const long long tq = t * a.qs, tk = t * a.ks;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long t = base + u * step + s.ti;
-      on[u] = s.active && t < a.tokens;
+    for (int i = 0; i < HU; ++i)
+      ring.copy(ahead, i * V,
+                on && hd[i].row >= 0 ? hd[i].row_at(static_cast<const T*>(a.q), static_cast<const T*>(a.k), tq, tk) : nullptr, a.q, a.d);
+    ring.commit();
+  };
+  const long long first = (long long)(blockIdx.x / a.nch) * a.tpi;
 #pragma unroll
-      for (int i = 0; i < HU; ++i) raw[u][i] = on[u] && hd[i].on ? load_raw(hd[i].x + t * hd[i].xs) : zero_raw<T>();
+  for (int k = 0; k < NS - 1; ++k) fetch(k, first + k * step + s.ti);
+  // the token at hand's turn; the next one's, under way; the positions of the one after that
+  Turn<LPR, SPLIT> after = turn;
+  int p[3], pn[3];
+  const long long t0 = first + s.ti;
+  bool on = s.active && t0 < a.tokens && positions(a, t0, p);
+  bool onn = s.active && t0 + step < a.tokens && positions(a, t0 + step, pn);
+  if (on) turn.angles(a, p);
+  for (long long base = first; base < a.tokens; base += step) {
+    const long long t = base + s.ti;
+    if (onn) after.angles(a, pn);
+    const bool ona = s.active && t + 2 * step < a.tokens && positions(a, t + 2 * step, pn);
+    fetch(NS - 1, t + (NS - 1) * step);
+    ring.wait();
+    const long long oq = t * dq, ok = t * dk;
+#pragma unroll
+    for (int i = 0; i < HU; ++i) {
+      float x[8], ss = 0.f;
+      expand(ring.template read<T>(i * V), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, a.eps));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= rstd * hd[i].w[e];
+      turn.apply(x, 1.f);
+      if (on && hd[i].on) store8(hd[i].at(static_cast<T*>(a.qo), static_cast<T*>(a.ko), oq, ok), x);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) on[u] = on[u] && positions(a, base + u * step + s.ti, p[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long t = base + u * step + s.ti;
-      if (on[u]) turn.angles(a, p[u]);
-#pragma unroll
-      for (int i = 0; i < HU; ++i) {
-        float x[8], ss = 0.f;
-        expand(raw[u][i], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, a.eps));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= rstd * hd[i].w[e];
-        turn.apply(x, 1.f);
-        if (on[u] && hd[i].on) store8(hd[i].o + t * hd[i].os, x);
-      }
-    }
+    ring.next();
+    turn.take(after);
+    on = onn;
+    onn = ona;
   }
 }
 
-template <typename T, typename G, int LPR, bool SPLIT, int HU, int U>
+template <typename T, typename G, int LPR, bool SPLIT, int HU>
 __global__ void __launch_bounds__(kThreads, 2) k_qk_bwd(const QkDev a) {
+  constexpr int NS = bwd_stages<T, G, HU>(), V = sizeof(T) / 2, VG = sizeof(G) / 2, NV = V + VG;
+  extern __shared__ uint4 qk_smem[];
+  Ring<HU * NV, NS, LPR> ring(qk_smem);
   const Slot<LPR, HU> s(a);
-  Head<T> hd[HU];
+  Head hd[HU];
   float acc[HU][8];
 #pragma unroll
   for (int i = 0; i < HU; ++i) {
@@ -273,86 +350,89 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_bwd(const QkDev a) {
     for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
   }
   Turn<LPR, SPLIT> turn(a, s.li, threadIdx.x & 31);
-  const long long step = (long long)a.gx * a.tpi;
+  const long long step = (long long)a.gx * a.tpi, dq = (long long)a.Hq * a.d, dk = (long long)(a.Ht - a.Hq) * a.d;
   const float inv_d = 1.0f / (float)a.d;
-  for (long long base = (long long)(blockIdx.x / a.nch) * a.tpi; base < a.tokens; base += U * step) {
-    Raw<T> rx[U][HU];
-    Raw<G> rg[U][HU];
-    int p[U][3];
-    bool on[U], in[U];
+  auto fetch = [&](int ahead, long long t) {
+    const bool on = s.row && t < a.tokens;
+    const long long tq = t * a.qs, tk = t * a.ks, oq = t * dq, ok = t * dk;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long t = base + u * step + s.ti;
-      in[u] = s.active && t < a.tokens;
-#pragma unroll
-      for (int i = 0; i < HU; ++i) {
-        const bool ld = in[u] && hd[i].on;
-        rx[u][i] = ld ? load_raw(hd[i].x + t * hd[i].xs) : zero_raw<T>();
-        rg[u][i] = ld ? load_raw(static_cast<const G*>(hd[i].isq ? a.gq : a.gk) + hd[i].off + t * hd[i].os) : zero_raw<G>();
-      }
+    for (int i = 0; i < HU; ++i) {
+      const bool ld = on && hd[i].row >= 0;
+      ring.copy(ahead, i * NV, ld ? hd[i].row_at(static_cast<const T*>(a.q), static_cast<const T*>(a.k), tq, tk) : nullptr, a.q, a.d);
+      ring.copy(ahead, i * NV + V, ld ? hd[i].row_at(static_cast<const G*>(a.gq), static_cast<const G*>(a.gk), oq, ok) : nullptr, a.q,
+                a.d);
     }
+    ring.commit();
+  };
+  const long long first = (long long)(blockIdx.x / a.nch) * a.tpi;
 #pragma unroll
-    for (int u = 0; u < U; ++u) on[u] = in[u] && positions(a, base + u * step + s.ti, p[u]);
+  for (int k = 0; k < NS - 1; ++k) fetch(k, first + k * step + s.ti);
+  for (long long base = first; base < a.tokens; base += step) {
+    const long long t = base + s.ti;
+    int p[3];
+    const bool in = s.active && t < a.tokens, on = in && positions(a, t, p);
+    if (on) turn.angles(a, p);
+    fetch(NS - 1, t + (NS - 1) * step);
+    ring.wait();
+    const long long oq = t * dq, ok = t * dk;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long t = base + u * step + s.ti;
-      if (on[u]) turn.angles(a, p[u]);
+    for (int i = 0; i < HU; ++i) {
+      float x[8], g[8], ss = 0.f, dot = 0.f;
+      expand(ring.template read<T>(i * NV), x);
+      expand(ring.template read<G>(i * NV + V), g);
+      if (!on) {
+        // a skipped token's output does not depend on its input: its gradient is zero, whatever the two arrays hold there
 #pragma unroll
-      for (int i = 0; i < HU; ++i) {
-        float x[8], g[8], ss = 0.f, dot = 0.f;
-        expand(rx[u][i], x);
-        expand(rg[u][i], g);
-        if (!on[u]) {
-          // a skipped token's output does not depend on its input: its gradient is zero, whatever the two arrays hold there
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = g[e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        turn.apply(g, -1.f);
-        const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, a.eps));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= rstd;
-          acc[i][e] = fmaf(g[e], x[e], acc[i][e]);
-          g[e] *= hd[i].w[e];
-          dot = fmaf(g[e], x[e], dot);
-        }
-        dot = row_sum<LPR>(dot) * inv_d;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = rstd * fmaf(-x[e], dot, g[e]);
-        if (in[u] && hd[i].on) store8(hd[i].o + t * hd[i].os, g);
+        for (int e = 0; e < 8; ++e) x[e] = g[e] = 0.f;
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      turn.apply(g, -1.f);
+      const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, a.eps));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] *= rstd;
+        acc[i][e] = fmaf(g[e], x[e], acc[i][e]);
+        g[e] *= hd[i].w[e];
+        dot = fmaf(g[e], x[e], dot);
+      }
+      dot = row_sum<LPR>(dot) * inv_d;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = rstd * fmaf(-x[e], dot, g[e]);
+      if (in && hd[i].on) store8(hd[i].at(static_cast<T*>(a.qo), static_cast<T*>(a.ko), oq, ok), g);
     }
+    ring.next();
   }
   if (a.part == nullptr) return;
-  // the block's sums: columns c of the LPR lanes' 8 LPR, slot after slot
-  __shared__ float buf[kThreads * 8];
-  constexpr int W = 8 * LPR, SLOTS = kThreads / LPR;
+  // the block's sums: columns c of the LPR lanes' 8 LPR, slot after slot, in the ring's memory
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  static_assert(bwd_smem<T, G, HU>() >= (size_t)HU * kThreads * 8 * sizeof(float), "the ring holds the sums");
+  float* buf = reinterpret_cast<float*>(qk_smem);
+  constexpr int W = 8 * LPR, PLANE = kThreads * 8;
   const int blk = blockIdx.x / a.nch, chunk = blockIdx.x % a.nch;
-  float sum[2] = {0.f, 0.f};  // shared weights: queries, keys
 #pragma unroll
-  for (int i = 0; i < HU; ++i) {
-    __syncthreads();
-    store8(buf + threadIdx.x * 8, acc[i]);
-    __syncthreads();
-    if (a.per_head) {
-      for (int j = threadIdx.x; j < a.hc * W; j += kThreads) {
-        const int hs = j / W, c = j % W, head = chunk * a.hc * HU + hs + i * a.hc;
-        float v = 0.f;
-        for (int t = 0; t < a.tpi; ++t) v += buf[(t * a.hc + hs) * W + c];
-        if (head < a.Ht && c < a.d) a.part[((long long)blk * a.Ht + head) * a.d + c] = v;
-      }
-    } else if (threadIdx.x < W) {
-      for (int sl = 0; sl < SLOTS && sl < a.hc * a.tpi; ++sl) {
-        const int head = chunk * a.hc * HU + sl % a.hc + i * a.hc;
-        if (head < a.Ht) sum[head < a.Hq ? 0 : 1] += buf[sl * W + threadIdx.x];
-      }
+  for (int i = 0; i < HU; ++i) store8(buf + i * PLANE + threadIdx.x * 8, acc[i]);
+  __syncthreads();
+  if (a.per_head) {
+    for (int j = threadIdx.x; j < HU * a.hc * W; j += blockDim.x) {
+      const int c = j % W, h = j / W, hs = h % a.hc, head = chunk * a.hc * HU + h;  // h = hs + i hc
+      float v = 0.f;
+      for (int t = 0; t < a.tpi; ++t) v += buf[h / a.hc * PLANE + (t * a.hc + hs) * W + c];
+      if (head < a.Ht && c < a.d) a.part[((long long)blk * a.Ht + head) * a.d + c] = v;
     }
-  }
-  if (!a.per_head && threadIdx.x < W && threadIdx.x < a.d) {
+  } else {
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+      float sum[2] = {0.f, 0.f};  // queries, keys
+      for (int i = 0; i < HU; ++i)
+        for (int sl = 0; sl < a.hc * a.tpi; ++sl) {
+          const int head = chunk * a.hc * HU + sl % a.hc + i * a.hc;
+          if (head < a.Hq) sum[0] += buf[i * PLANE + sl * W + c];
+          else if (head < a.Ht) sum[1] += buf[i * PLANE + sl * W + c];
+        }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) a.part[(((long long)blk * a.nch + chunk) * 2 + k) * a.d + threadIdx.x] = sum[k];
+      for (int k = 0; k < 2; ++k) a.part[(((long long)blk * a.nch + chunk) * 2 + k) * a.d + c] = sum[k];
+    }
   }
 }
 
@@ -413,8 +493,9 @@ bool plan(const vdn_qk_cfg& c, QkDev& a, int hu, int resident) {
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return false;
   qk_slots(c, hu, &a.hc, &a.tpi, &a.nch);
+  a.threads = (a.hc * a.tpi * lanes_per_row(c.d) + 31) / 32 * 32;
   const long long steps = (c.tokens + a.tpi - 1) / a.tpi;
-  long long gx = (long long)resident * sms / a.nch;
+  long long gx = (long long)resident * (kThreads / a.threads) * sms / a.nch;
   if (gx > qk_max_blocks(a.nch)) gx = qk_max_blocks(a.nch);
   if (gx < 1) gx = 1;
   a.gx = (int)(steps < gx ? steps : gx);
@@ -439,30 +520,35 @@ QkDev device_args(const vdn_qk_cfg& c, const vdn_qk_args& in) {
   return a;
 }
 
+template <typename K>
+cudaError_t go(K kern, const QkDev& a, size_t smem, unsigned grid, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, a.threads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int LPR, int HU>
+cudaError_t go_fwd(const QkDev& a, bool split, unsigned grid, cudaStream_t s) {
+  return split ? go(k_qk_fwd<T, LPR, true, HU>, a, fwd_smem<T, HU>(), grid, s)
+               : go(k_qk_fwd<T, LPR, false, HU>, a, fwd_smem<T, HU>(), grid, s);
+}
+template <typename T, typename G, int LPR, int HU>
+cudaError_t go_bwd(const QkDev& a, bool split, unsigned grid, cudaStream_t s) {
+  return split ? go(k_qk_bwd<T, G, LPR, true, HU>, a, bwd_smem<T, G, HU>(), grid, s)
+               : go(k_qk_bwd<T, G, LPR, false, HU>, a, bwd_smem<T, G, HU>(), grid, s);
+}
 template <typename T, int LPR>
-void run_fwd(const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
-  constexpr int HU = LPR < 8 ? 1 : sizeof(T) == 2 ? 3 : 2, U = sizeof(T) == 2 ? 4 : 2;
-  if (hu > 1) {
-    if (split) k_qk_fwd<T, LPR, true, HU, 1><<<grid, kThreads, 0, s>>>(a);
-    else k_qk_fwd<T, LPR, false, HU, 1><<<grid, kThreads, 0, s>>>(a);
-  } else {
-    if (split) k_qk_fwd<T, LPR, true, 1, U><<<grid, kThreads, 0, s>>>(a);
-    else k_qk_fwd<T, LPR, false, 1, U><<<grid, kThreads, 0, s>>>(a);
-  }
+cudaError_t run_fwd(const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
+  constexpr int HU = LPR < 8 ? 1 : sizeof(T) == 2 ? 3 : 2;
+  return hu > 1 ? go_fwd<T, LPR, HU>(a, split, grid, s) : go_fwd<T, LPR, 1>(a, split, grid, s);
 }
 template <typename T, typename G, int LPR>
-void run_bwd(const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
-  constexpr int HU = LPR < 8 ? 1 : sizeof(T) == 2 ? 3 : 2, U = sizeof(T) == 2 ? 3 : 2;
-  if (hu > 1) {
-    if (split) k_qk_bwd<T, G, LPR, true, HU, 1><<<grid, kThreads, 0, s>>>(a);
-    else k_qk_bwd<T, G, LPR, false, HU, 1><<<grid, kThreads, 0, s>>>(a);
-  } else {
-    if (split) k_qk_bwd<T, G, LPR, true, 1, U><<<grid, kThreads, 0, s>>>(a);
-    else k_qk_bwd<T, G, LPR, false, 1, U><<<grid, kThreads, 0, s>>>(a);
-  }
+cudaError_t run_bwd(const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
+  constexpr int HU = LPR < 8 ? 1 : sizeof(T) == 2 ? 3 : 2;
+  return hu > 1 ? go_bwd<T, G, LPR, HU>(a, split, grid, s) : go_bwd<T, G, LPR, 1>(a, split, grid, s);
 }
 template <typename T>
-void fwd_lanes(int lpr, const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
+cudaError_t fwd_lanes(int lpr, const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
   switch (lpr) {
     case 2: return run_fwd<T, 2>(a, split, hu, grid, s);
     case 4: return run_fwd<T, 4>(a, split, hu, grid, s);
@@ -472,7 +558,7 @@ void fwd_lanes(int lpr, const QkDev& a, bool split, int hu, unsigned grid, cudaS
   }
 }
 template <typename T, typename G>
-void bwd_lanes(int lpr, const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
+cudaError_t bwd_lanes(int lpr, const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {
   switch (lpr) {
     case 2: return run_bwd<T, G, 2>(a, split, hu, grid, s);
     case 4: return run_bwd<T, G, 4>(a, split, hu, grid, s);
@@ -496,9 +582,8 @@ cudaError_t launch_qk_fwd(const vdn_qk_cfg& c, const vdn_qk_args& in, cudaStream
   if (!plan(c, a, hu, 3)) return cudaErrorInvalidDevice;
   const unsigned grid = (unsigned)a.gx * a.nch;
   const bool split = c.pairing == VDN_PAIR_SPLIT;
-  if (c.dtype == VDN_BF16) fwd_lanes<__nv_bfloat16>(lanes_per_row(c.d), a, split, hu, grid, s);
-  else fwd_lanes<float>(lanes_per_row(c.d), a, split, hu, grid, s);
-  return cudaGetLastError();
+  return c.dtype == VDN_BF16 ? fwd_lanes<__nv_bfloat16>(lanes_per_row(c.d), a, split, hu, grid, s)
+                             : fwd_lanes<float>(lanes_per_row(c.d), a, split, hu, grid, s);
 }
 
 cudaError_t launch_qk_bwd(const vdn_qk_cfg& c, const vdn_qk_args& in, const vdn_qk_grads& g, cudaStream_t s) {
@@ -511,10 +596,9 @@ cudaError_t launch_qk_bwd(const vdn_qk_cfg& c, const vdn_qk_args& in, const vdn_
   const unsigned grid = (unsigned)a.gx * a.nch;
   const bool split = c.pairing == VDN_PAIR_SPLIT;
   const int lpr = lanes_per_row(c.d);
-  if (c.dtype == VDN_F32) bwd_lanes<float, float>(lpr, a, split, hu, grid, s);
-  else if (c.grad_dtype == VDN_F32) bwd_lanes<__nv_bfloat16, float>(lpr, a, split, hu, grid, s);
-  else bwd_lanes<__nv_bfloat16, __nv_bfloat16>(lpr, a, split, hu, grid, s);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = c.dtype == VDN_F32        ? bwd_lanes<float, float>(lpr, a, split, hu, grid, s)
+                        : c.grad_dtype == VDN_F32 ? bwd_lanes<__nv_bfloat16, float>(lpr, a, split, hu, grid, s)
+                                                  : bwd_lanes<__nv_bfloat16, __nv_bfloat16>(lpr, a, split, hu, grid, s);
   if (e != cudaSuccess || !want) return e;
   const int sets = c.per_head ? a.Ht : 2;
   k_qk_dw<<<dim3((c.d + 31) / 32, sets), 1024, 0, s>>>(a.part, g.dwq, c.Hk > 0 ? g.dwk : nullptr, c.per_head ? a.gx : a.gx * a.nch,
