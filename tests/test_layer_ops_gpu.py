@@ -80,7 +80,7 @@ def qk_forward_check(op, a, on, dt, out):
             p = torch.arange(a[key].shape[0], device="cuda", dtype=torch.int32).unsqueeze(1)
         else:
             p = torch.where(on.unsqueeze(1), a["pos"], 0)
-        pair = "interleaved" if op.base["pairing"] == L.PAIR_INTERLEAVED else "split"
+        pair = "interleaved" if op.pairing == L.PAIR_INTERLEAVED else "split"
         want = R.qk_norm_rope(a[key], a["w" + key], a["table"], p, op.rot, pair, op.sections, 1e-6)
         # an element is two products of values with a few roundings each; a pair's size bounds both
         size = want.abs().amax(-1, keepdim=True) * 2
@@ -112,7 +112,7 @@ def test_qk_norm_rope_backward(cuda_ok, case, gdtype):
             up[k][~on] = math.inf
     got = op.backward(a["q"], a["k"], a["wq"], a["wk"], a["table"], up["q"], up["k"], a["pos"])
     p = torch.where(on.unsqueeze(1), a["pos"], 0)[on]
-    pair = "interleaved" if op.base["pairing"] == L.PAIR_INTERLEAVED else "split"
+    pair = "interleaved" if op.pairing == L.PAIR_INTERLEAVED else "split"
     for k in "qk":
         if a[k] is None:
             assert "d" + k not in got and "dw" + k not in got

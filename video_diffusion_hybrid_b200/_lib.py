@@ -326,7 +326,7 @@ def make_args(q, k, v, beta, alpha, gate_sm, gate_lin, y, workspace, workspace_b
 def _stream_handle(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -6,6 +6,9 @@ memory and the current stream.
 """
 from __future__ import annotations
 
+import ctypes
+import math
+
 import numpy as np
 import torch
 
@@ -216,7 +219,7 @@ def _need(t, name: str, shape, dtype, device) -> None:
     """A dense tensor of this shape, type and device (None passes)."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
@@ -225,19 +228,20 @@ def _head_rows(t: torch.Tensor, name: str, lead: tuple, H: int, d: int, dtype, d
     """Checks a [*lead, H, d] tensor whose head rows are dense and whose tokens
     lie one stride apart (a slice of a packed projection); returns that stride
     in elements."""
-    if tuple(t.shape) != (*lead, H, d) or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name}: expected {dtype} {(*lead, H, d)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    shape, strides = t.shape, t.stride()
+    if shape != (*lead, H, d) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {(*lead, H, d)} on {device}, got {t.dtype} {tuple(shape)} on {t.device}")
     # the stride of an axis of size one says nothing
-    if (d > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != d):
-        raise ValueError(f"{name}: the head rows have to be dense, got strides {t.stride()}")
+    if (d > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != d):
+        raise ValueError(f"{name}: the head rows have to be dense, got strides {strides}")
     stride, span = None, 0
-    for size, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
-        if size == 1:
+    for i in range(len(shape) - 3, -1, -1):
+        if shape[i] == 1:
             continue
-        if st < H * d or (stride is not None and st != span):
-            raise ValueError(f"{name}: the tokens have to lie one stride apart, got strides {t.stride()}")
-        stride = st if stride is None else stride
-        span = st * size
+        if strides[i] < H * d or (stride is not None and strides[i] != span):
+            raise ValueError(f"{name}: the tokens have to lie one stride apart, got strides {strides}")
+        stride = strides[i] if stride is None else stride
+        span = strides[i] * shape[i]
     return H * d if stride is None else stride
 
 
@@ -249,6 +253,7 @@ class _Streamed:
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._like = torch.empty(0, device=self.device)
 
     def _call(self, fn, *args, stream=None):
         if torch.cuda.current_device() == self.device.index:
@@ -261,7 +266,7 @@ class _Streamed:
         handed out again before that stream's work is done.  Scratch is new on
         every call, so calls on several streams and captured graphs do not share it."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self._like.new_empty(shape, dtype=dtype)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
         with torch.cuda.stream(stream):
@@ -288,33 +293,29 @@ class QKNormRope(_Streamed):
         pair = {"interleaved": L.PAIR_INTERLEAVED, "split": L.PAIR_SPLIT}
         if pairing not in pair or not 1 <= len(self.sections) <= 3:
             raise L.VdnError(L.VDN_ERR_INVALID_ARG, "QKNormRope")
-        self.axes = len(self.sections)
-        self.base = dict(Hq=Hq, Hk=Hk, d=d, rot=self.rot, pairing=pair[pairing], axes=self.axes,
-                         per_head=int(per_head), eps=eps)
+        self.axes, self.pairing, self.eps = len(self.sections), pair[pairing], eps
+        self.c_sections = (ctypes.c_int * 3)(*self.sections)
+        self.wq_shape, self.wk_shape = ((Hq, d), (Hk, d)) if per_head else ((d,), (d,))
 
     def _cfg_args(self, q, k, wq, wk, table, pos):
-        lead, dt = tuple(q.shape[:-2]), q.dtype
-        qs = _head_rows(q, "q", lead, self.Hq, self.d, dt, self.device)
-        ks = _head_rows(k, "k", lead, self.Hk, self.d, dt, self.device) if self.Hk else 0
-        n = 1
-        for s in lead:
-            n *= s
-        f32 = torch.float32
-        _need(wq, "wq", (self.Hq, self.d) if self.per_head else (self.d,), f32, self.device)
-        _need(wk, "wk", (self.Hk, self.d) if self.per_head else (self.d,), f32, self.device)
+        lead, dt, dev = q.shape[:-2], q.dtype, self.device
+        qs = _head_rows(q, "q", lead, self.Hq, self.d, dt, dev)
+        ks = _head_rows(k, "k", lead, self.Hk, self.d, dt, dev) if self.Hk else 0
+        _need(wq, "wq", self.wq_shape, torch.float32, dev)
+        _need(wk, "wk", self.wk_shape, torch.float32, dev)
         rows = 0
         if self.rot:
+            if table is None:
+                raise ValueError("table: the rotation needs one")
             rows = table.shape[0]
-            _need(table, "table", (rows, self.rot // 2, 2), f32, self.device)
+            _need(table, "table", (rows, self.rot // 2, 2), torch.float32, dev)
         if pos is not None:
-            _need(pos, "pos", lead if self.axes == 1 and pos.dim() == len(lead) else (*lead, self.axes), torch.int32, self.device)
+            _need(pos, "pos", lead if self.axes == 1 and pos.dim() == len(lead) else (*lead, self.axes), torch.int32, dev)
             rows = rows or 2**31 - 1
-        cfg = L.QkCfg(tokens=n, table_rows=rows, dtype=_dtype_of(q), q_stride=qs, k_stride=ks, **self.base)
-        for i, s in enumerate(self.sections):
-            cfg.sections[i] = s
-        args = L.QkArgs(q=q.data_ptr(), k=k.data_ptr() if self.Hk else None, wq=L._ptr(wq), wk=L._ptr(wk),
-                        table=table.data_ptr() if self.rot else None, pos=L._ptr(pos))
-        return cfg, args
+        cfg = L.QkCfg(math.prod(lead), self.Hq, self.Hk, self.d, self.rot, self.pairing, self.axes, self.c_sections, rows,
+                      int(self.per_head), _dtype_of(q), 0, self.eps, qs, ks)
+        return cfg, L.QkArgs(q.data_ptr(), k.data_ptr() if self.Hk else None, L._ptr(wq), L._ptr(wk),
+                             table.data_ptr() if self.rot else None, L._ptr(pos))
 
     def __call__(self, q, k, wq=None, wk=None, table=None, pos=None, out=None, stream=None):
         """(q_out, k_out), dense, of q's type; `out`: a pair of tensors to write."""
@@ -338,10 +339,9 @@ class QKNormRope(_Streamed):
             _need(dk_out, "dk_out", k.shape, dq_out.dtype, self.device)
         ws = self._new(L.vdn_qk_norm_rope_bwd_workspace_size(cfg), torch.uint8, stream)
         new = lambda shape, dt: self._new(shape, dt, stream)  # noqa: E731
-        wshape = (lambda h: (h, self.d)) if self.per_head else (lambda h: (self.d,))
-        g = {"dq": new(q.shape, q.dtype), "dwq": new(wshape(self.Hq), torch.float32)}
+        g = {"dq": new(q.shape, q.dtype), "dwq": new(self.wq_shape, torch.float32)}
         if self.Hk:
-            g["dk"], g["dwk"] = new(k.shape, q.dtype), new(wshape(self.Hk), torch.float32)
+            g["dk"], g["dwk"] = new(k.shape, q.dtype), new(self.wk_shape, torch.float32)
         gr = L.QkGrads(L._ptr(dq_out), L._ptr(dk_out) if self.Hk else None, L._ptr(g["dq"]), L._ptr(g.get("dk")),
                        L._ptr(g["dwq"]), L._ptr(g.get("dwk")), ws.data_ptr(), ws.numel())
         self._call(L.vdn_qk_norm_rope_bwd, cfg, args, gr, stream=stream)

@@ -120,6 +120,20 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&v)[3
                                                       pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
 }
 
+// 32 columns of int32 sums to scaled values: (sum rs) col_scale + bias, columns in fours (N is a multiple of 16)
+__device__ __forceinline__ void scale_s8(float (&v)[32], const GemmArgs& g, int n, int cols, float rs) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    if (i >= cols) continue;
+    const float4 w = __ldg(reinterpret_cast<const float4*>(g.col_scale + n + i));
+    const float4 b = g.bias ? __ldg(reinterpret_cast<const float4*>(g.bias + n + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[i] = fmaf((float)__float_as_int(v[i]) * rs, w.x, b.x);
+    v[i + 1] = fmaf((float)__float_as_int(v[i + 1]) * rs, w.y, b.y);
+    v[i + 2] = fmaf((float)__float_as_int(v[i + 2]) * rs, w.z, b.z);
+    v[i + 3] = fmaf((float)__float_as_int(v[i + 3]) * rs, w.w, b.w);
+  }
+}
+
 // K_BF16: A bf16 [M, K] (K-major), B = W bf16 [K, N] (N contiguous: MN-major).
 // K_FP8, K_S8: A [M, K], B = W^T [N, K], one byte each (both K-major).
 template <Kind KIND, typename To>
@@ -260,20 +274,7 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
           for (int i = 0; i < 32; ++i) v[i] *= sc;
         }
         const int cols = g.N - (n0 + 32 * c);
-        if (KIND == K_S8) {
-          // columns in fours: N is a multiple of 16
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            if (i >= cols) continue;
-            const float4 w = __ldg(reinterpret_cast<const float4*>(g.col_scale + n0 + 32 * c + i));
-            const float4 b = g.bias ? __ldg(reinterpret_cast<const float4*>(g.bias + n0 + 32 * c + i))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[i] = fmaf((float)__float_as_int(v[i]) * rs, w.x, b.x);
-            v[i + 1] = fmaf((float)__float_as_int(v[i + 1]) * rs, w.y, b.y);
-            v[i + 2] = fmaf((float)__float_as_int(v[i + 2]) * rs, w.z, b.z);
-            v[i + 3] = fmaf((float)__float_as_int(v[i + 3]) * rs, w.w, b.w);
-          }
-        }
+        if (KIND == K_S8) scale_s8(v, g, n0 + 32 * c, cols, rs);
         if (valid && cols > 0) store_row(out + row * g.N + n0 + 32 * c, v, cols);
       }
       tc_fence_before();
@@ -285,6 +286,118 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
   cluster_sync_all();  // no CTA leaves while its peer may still touch its memory or barriers
   tc_fence_after();
   if (warp == 1) tmem_free2(tmem, kCols);
+}
+
+// ------------------------------------------------------ few output tiles --
+// The 8-bit product where the pairs' 256 x 256 tiles would leave most SMs idle:
+// 128 x TNS tiles, one for each CTA, the same stages and roles on one SM.
+// Bound by the latency of its one tile (loads, K blocks, epilogue) and, with
+// few rows, by the read of the weight.
+constexpr int STS = 8;  // stages
+template <int TNS> constexpr uint32_t small_stage() { return ABYTES + TNS * KBYTES; }
+template <int TNS> constexpr size_t small_smem() { return 1024 + (size_t)STS * small_stage<TNS>() + 32 * 8 + 16; }
+
+__device__ __forceinline__ void mma1_s8_w(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+
+template <int TNS, typename To>
+__global__ void __launch_bounds__(kThreadsG, 1)
+k_gemm_s8_small(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb) {
+  enum { B_FULL = 0, B_EMPTY = STS, B_DONE = 2 * STS, NBARS };
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + STS * small_stage<TNS>());
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Ctl ctl{abort_flag, g_proj_status, (unsigned)VDN_TAG_PROJ, 0};
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int m0 = (int)(blockIdx.x / g.tiles_n) * TM, n0 = (int)(blockIdx.x % g.tiles_n) * TNS;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), TNS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp == 0) {
+    int issued = 0;
+    for (int kb = 0; kb < g.nkb; ++kb) {
+      const int s = kb % STS;
+      if (kb >= STS && !mbar_wait_warp(bar(B_EMPTY + s), (kb / STS - 1) & 1, ctl)) break;
+      if (lane == 0) {
+        const uint32_t sa = smem_u32(sm + s * small_stage<TNS>());
+        mbar_expect_tx(bar(B_FULL + s), small_stage<TNS>());
+        tma_load_2d(sa, &tma, bar(B_FULL + s), kb * KBYTES, m0);
+        tma_load_2d(sa + ABYTES, &tmb, bar(B_FULL + s), kb * KBYTES, n0);
+      }
+      issued = kb + 1;
+    }
+    if (lane == 0)
+      for (int kb = issued > STS ? issued - STS : 0; kb < issued; ++kb) mbar_drain(bar(B_FULL + kb % STS), (kb / STS) & 1);
+  } else if (warp == 1) {
+    const uint32_t el = elect_one();
+    const uint64_t a0 = sdesc(smem_u32(sm), 16, 1024), b0 = sdesc(smem_u32(sm + ABYTES), 16, 1024);
+    for (int kb = 0; kb < g.nkb; ++kb) {
+      const int s = kb % STS;
+      if (!mbar_wait_warp(bar(B_FULL + s), (kb / STS) & 1, ctl)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma1_s8_w(tmem, dadd(a0, s * small_stage<TNS>() + k * 32), dadd(b0, s * small_stage<TNS>() + k * 32), idesc_s8(TM, TNS),
+                  (kb | k) ? 1u : 0u, el);
+      mma_commit_w(bar(B_EMPTY + s), el);
+    }
+    mma_commit_w(bar(B_DONE), el);
+    mbar_drain(bar(B_DONE), 0);
+  } else if (warp >= 4) {
+    const int row = m0 + (warp & 3) * 32 + lane;
+    const bool valid = row < g.M;
+    const float rs = valid ? __ldg(g.row_scale + row) : 0.f;
+    if (mbar_wait_warp(bar(B_DONE), 0, ctl) && *abort_flag == 0) {
+      tc_fence_after();
+      To* out = static_cast<To*>(g.out);
+#pragma unroll
+      for (int c = 0; c < TNS / 32; ++c) {
+        const int cols = g.N - (n0 + 32 * c);
+        if (cols <= 0) continue;  // uniform
+        float v[32];
+        tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 32 * c, v);
+        tmem_wait_ld();
+        scale_s8(v, g, n0 + 32 * c, cols, rs);
+        if (valid) store_row(out + (long long)row * g.N + n0 + 32 * c, v, cols);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free(tmem, TNS);
+}
+
+template <int TNS, typename To>
+vdn_status launch_small(int M, int K, int N, const void* a, const void* w, void* out, cudaStream_t s, GemmArgs g) {
+  CUtensorMap ma, mb;
+  if (!make_matrix_map_u8(&ma, a, M, K, TM) || !make_matrix_map_u8(&mb, w, N, K, TNS)) return VDN_ERR_CUDA;
+  g.M = M; g.N = N; g.K = K;
+  g.tiles_n = (N + TNS - 1) / TNS;
+  g.tiles = g.tiles_n * ((M + TM - 1) / TM);
+  g.nkb = (K + KBYTES - 1) / KBYTES;
+  g.out = out;
+  auto kern = k_gemm_s8_small<TNS, To>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)small_smem<TNS>()) != cudaSuccess) return VDN_ERR_CUDA;
+  kern<<<g.tiles, kThreadsG, small_smem<TNS>(), s>>>(g, ma, mb);
+  return cudaGetLastError() == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
 
 constexpr size_t gemm_smem() { return 1024 + (size_t)ST * STAGE + 32 * 8 + 16; }
@@ -349,14 +462,21 @@ vdn_status out_proj(int M, int K, int N, int out_dtype, const void* y, const voi
 }
 
 vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
-                   const float* w_scale, const float* bias, void* out, cudaStream_t s) {
-  if (!clear_status(s)) return VDN_ERR_CUDA;
+                   const float* w_scale, const float* bias, void* out, bool clear, cudaStream_t s) {
+  if (clear ? !clear_status(s) : !encode_fn()) return VDN_ERR_CUDA;
   GemmArgs g{};
   g.row_scale = a_scale;
   g.col_scale = w_scale;
   g.bias = bias;
-  return out_dtype == VDN_BF16 ? launch<K_S8, __nv_bfloat16>(M, K, N, a, w, out, s, g)
-                               : launch<K_S8, float>(M, K, N, a, w, out, s, g);
+  const bool bf = out_dtype == VDN_BF16;
+  auto tiles = [&](int tm, int tn) { return (long long)((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+  // Fewer 256 x 256 tiles than CTA pairs: smaller tiles, and narrower ones still while they fit on the SMs at once.
+  if (tiles(2 * TM, TN) < 74) {
+    if (tiles(TM, 32) <= 148)
+      return bf ? launch_small<32, __nv_bfloat16>(M, K, N, a, w, out, s, g) : launch_small<32, float>(M, K, N, a, w, out, s, g);
+    return bf ? launch_small<64, __nv_bfloat16>(M, K, N, a, w, out, s, g) : launch_small<64, float>(M, K, N, a, w, out, s, g);
+  }
+  return bf ? launch<K_S8, __nv_bfloat16>(M, K, N, a, w, out, s, g) : launch<K_S8, float>(M, K, N, a, w, out, s, g);
 }
 
 uint32_t* status_of_proj() {

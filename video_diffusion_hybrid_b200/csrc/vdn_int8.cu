@@ -78,7 +78,8 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const Scale& c) {
 // between the maximum and the codes (one read of x); longer rows are read twice.
 template <typename T, int TPR, int VPT>
 __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, int rows, int cols, uint2* __restrict__ q,
-                                                       float* __restrict__ scale) {
+                                                       float* __restrict__ scale, uint32_t* status) {
+  if (status != nullptr && blockIdx.x == 0 && threadIdx.x < 2) status[threadIdx.x] = 0;
   const int t = threadIdx.x % TPR;
   const long long row = (long long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
   const bool on = row < rows;
@@ -125,10 +126,10 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
 }
 
 template <typename T>
-cudaError_t quantize(const T* x, int rows, int cols, uint2* q, float* scale, cudaStream_t s) {
+cudaError_t quantize(const T* x, int rows, int cols, uint2* q, float* scale, uint32_t* st, cudaStream_t s) {
   // a warp a row keeps up to 1024 columns in registers, a block a row 8192
-  if (cols <= 1024) k_quantize_rows<T, 32, 4><<<(rows + 7) / 8, 256, 0, s>>>(x, rows, cols, q, scale);
-  else k_quantize_rows<T, 256, 4><<<rows, 256, 0, s>>>(x, rows, cols, q, scale);
+  if (cols <= 1024) k_quantize_rows<T, 32, 4><<<(rows + 7) / 8, 256, 0, s>>>(x, rows, cols, q, scale, st);
+  else k_quantize_rows<T, 256, 4><<<rows, 256, 0, s>>>(x, rows, cols, q, scale, st);
   return cudaGetLastError();
 }
 
@@ -248,10 +249,11 @@ cudaError_t few_out(const vdn_int8_cfg& c, const vdn_int8_args& a, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_quantize_int8(const void* x, int dtype, int rows, int cols, void* q, float* scale, cudaStream_t s) {
+cudaError_t launch_quantize_int8(const void* x, int dtype, int rows, int cols, void* q, float* scale, uint32_t* status,
+                                 cudaStream_t s) {
   uint2* o = static_cast<uint2*>(q);
-  return dtype == VDN_BF16 ? quantize(static_cast<const __nv_bfloat16*>(x), rows, cols, o, scale, s)
-                           : quantize(static_cast<const float*>(x), rows, cols, o, scale, s);
+  return dtype == VDN_BF16 ? quantize(static_cast<const __nv_bfloat16*>(x), rows, cols, o, scale, status, s)
+                           : quantize(static_cast<const float*>(x), rows, cols, o, scale, status, s);
 }
 
 bool int8_few_supported(int M, int K, int N) { return M <= kFewRows && (size_t)M * K <= kFewSmem && N % NC == 0; }

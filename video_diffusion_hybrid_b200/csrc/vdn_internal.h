@@ -106,11 +106,13 @@ vdn_status out_proj(int M, int K, int N, int out_dtype, const void* y, const voi
                     const float* scales = nullptr);
 // device address of the projection's status words (library-owned), or null
 uint32_t* status_of_proj();
-// out = float(a w^T) a_scale[m] w_scale[n] + bias[n]: signed 8-bit codes a [M, K], w [N, K]
+// out = float(a w^T) a_scale[m] w_scale[n] + bias[n]: signed 8-bit codes a [M, K], w [N, K]; clear: its status words
+// first (else an earlier kernel of the stream has cleared them)
 vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
-                   const float* w_scale, const float* bias, void* out, cudaStream_t s);
-// codes and scale of every row of x (vdn_int8.cu)
-cudaError_t launch_quantize_int8(const void* x, int dtype, int rows, int cols, void* q, float* scale, cudaStream_t s);
+                   const float* w_scale, const float* bias, void* out, bool clear, cudaStream_t s);
+// codes and scale of every row of x (vdn_int8.cu); clears the two status words unless null
+cudaError_t launch_quantize_int8(const void* x, int dtype, int rows, int cols, void* q, float* scale, uint32_t* status,
+                                 cudaStream_t s);
 // the 8-bit linear layer for few rows, quantising x inside (x_scale == null) or taking codes
 bool int8_few_supported(int M, int K, int N);
 cudaError_t launch_int8_few(const vdn_int8_cfg& c, const vdn_int8_args& a, cudaStream_t s);

@@ -169,7 +169,6 @@ vdn_status vdn_cross_attn(const vdn_xattn_cfg* cfg, const vdn_xattn_args* args, 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const XDims d = xdims(cfg, args);
   const XArgs a = xargs(args, nullptr);
-  if (cudaMemsetAsync(a.status, 0, kAlign, s) != cudaSuccess) return VDN_ERR_CUDA;
   if (on_tensor_cores(cfg)) return launch_xattn_tc(d, a, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
   return launch_xattn_simt(d, a, cfg->dtype == VDN_BF16, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
@@ -184,7 +183,6 @@ vdn_status vdn_cross_attn_bwd(const vdn_xattn_cfg* cfg, const vdn_xattn_args* ar
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const XDims d = xdims(cfg, args);
   const XArgs a = xargs(args, g);
-  if (cudaMemsetAsync(a.status, 0, kAlign, s) != cudaSuccess) return VDN_ERR_CUDA;
   if (on_tensor_cores(cfg)) return launch_xattn_tc_bwd(d, a, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
   return launch_xattn_simt_bwd(d, a, cfg->dtype == VDN_BF16, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
@@ -202,7 +200,7 @@ vdn_status vdn_cross_attn_device_status(const void* workspace, vdn_stream_t stre
 vdn_status vdn_quantize_int8(const void* x, int x_dtype, int rows, int cols, void* q, float* scale, vdn_stream_t stream) {
   if (!ok_ptr(x, 16) || !ok_ptr(q, 16) || !ok_ptr(scale, 4) || !float_type(x_dtype)) return VDN_ERR_INVALID_ARG;
   if (rows < 1 || cols < 16 || cols % 16) return VDN_ERR_INVALID_ARG;
-  return launch_quantize_int8(x, x_dtype, rows, cols, q, scale, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_quantize_int8(x, x_dtype, rows, cols, q, scale, nullptr, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? VDN_OK : VDN_ERR_CUDA;
 }
 
@@ -225,11 +223,13 @@ vdn_status vdn_linear_int8(const vdn_int8_cfg* cfg, const vdn_int8_args* args, v
   if (cfg->x_dtype != VDN_I8) {
     char* ws = static_cast<char*>(args->workspace);
     float* sc = reinterpret_cast<float*>(ws + up((size_t)cfg->M * cfg->K));
-    if (launch_quantize_int8(args->x, cfg->x_dtype, cfg->M, cfg->K, ws, sc, s) != cudaSuccess) return VDN_ERR_CUDA;
+    uint32_t* status = status_of_proj();
+    if (!status || launch_quantize_int8(args->x, cfg->x_dtype, cfg->M, cfg->K, ws, sc, status, s) != cudaSuccess) return VDN_ERR_CUDA;
     codes = ws;
     scale = sc;
   }
-  return gemm_s8(cfg->M, cfg->K, cfg->N, cfg->out_dtype, codes, scale, args->w, args->w_scale, args->bias, args->out, s);
+  return gemm_s8(cfg->M, cfg->K, cfg->N, cfg->out_dtype, codes, scale, args->w, args->w_scale, args->bias, args->out,
+                 cfg->x_dtype == VDN_I8, s);
 }
 
 }  // extern "C"

@@ -116,6 +116,7 @@ template <int D> constexpr size_t bwd_smem() { return sizeof(float) * (4 * D * P
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThr) k_xattn(const XDims d, const XArgs a) {
+  clear_status(a.status);
   extern __shared__ __align__(16) float sm[];
   float *sQ = sm, *sK = sQ + D * PT, *sV = sK + D * PT, *sP = sV + BT * (D + 4);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(kThr) k_xattn(const XDims d, const XArgs a) {
 // Delta = <dO, o> of every query row: a warp a row
 template <typename T>
 __global__ void __launch_bounds__(256) k_xattn_delta(const T* __restrict__ y, const T* __restrict__ dy, float* __restrict__ delta,
-                                                     long long rows, int D) {
+                                                     long long rows, int D, uint32_t* status) {
+  clear_status(status);
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
   float s = 0.f;
@@ -320,7 +322,7 @@ template <typename T, int D>
 cudaError_t bwd(const XDims& d, const XArgs& a, cudaStream_t s) {
   const long long rows = (long long)d.B * d.Tq * d.H;
   float* delta = static_cast<float*>(a.scratch);
-  k_xattn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(static_cast<const T*>(a.y), static_cast<const T*>(a.dy), delta, rows, D);
+  k_xattn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(static_cast<const T*>(a.y), static_cast<const T*>(a.dy), delta, rows, D, a.status);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (!grow_smem(k_xattn_dq<T, D>, bwd_smem<D>()) || !grow_smem(k_xattn_dkv<T, D>, bwd_smem<D>())) return cudaErrorInvalidValue;

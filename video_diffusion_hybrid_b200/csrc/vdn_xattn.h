@@ -19,7 +19,7 @@ struct XArgs {
   float* lse;          // [B, Tq, H]; forward: written unless null; backward: read
   const void* dy;
   void *dq, *dk, *dv;
-  uint32_t* status;    // status words of the bounded waits
+  uint32_t* status;    // status words of the bounded waits; a call's first kernel clears them
   void* scratch;       // backward: behind the status words
 };
 
@@ -59,6 +59,11 @@ struct ItemPos {
     if (d2 >= g.r2) { d2 -= g.r2; ++d3; }
   }
 };
+
+// Clears the two status words: a call's first kernel does it as it starts, long before a bounded wait can run out.
+__device__ __forceinline__ void clear_status(uint32_t* status) {
+  if (blockIdx.x == 0 && threadIdx.x < 2) status[threadIdx.x] = 0;
+}
 
 // SIMT, float32 arithmetic: any type, d = 32, 64 or 128 (vdn_xattn.cu)
 cudaError_t launch_xattn_simt(const XDims& d, const XArgs& a, bool bf16, cudaStream_t s);

@@ -785,6 +785,7 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
 template <int D>
 __global__ void __launch_bounds__(256) k_xattn_delta_bf16(const XbDev x, long long rows) {
   constexpr int LR = D / 8, U = 4;  // U rows a thread, loads first
+  clear_status(x.status);
   const long long base = (long long)blockIdx.x * (256 / LR) * U + threadIdx.x / LR;
   const int li = threadIdx.x % LR;
   uint4 a[U], g[U];

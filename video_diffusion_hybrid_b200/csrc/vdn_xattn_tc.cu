@@ -169,6 +169,7 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
   const Ctl ctl{abort_flag, x.status, (unsigned)VDN_TAG_XATTN, 0};
   auto bar = [&](int i) { return smem_u32(bars + i); };
 
+  clear_status(x.status);
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i >= B_PFULL && i < B_OHALF ? 4 : 1);  // P: an arrival per softmax warp
     *abort_flag = 0;
