@@ -187,6 +187,12 @@ X = [  # B, Tq, L, H, Hkv, d, dtype, lens, strided
     (1, 333, 1500, 24, 1, 64, "bf16", None, False),
     (5, 40, 20, 9, 3, 128, "bf16", [20, 1, 7, 0, 100], True),
     (2, 33, 40, 2, 1, 32, "bf16", [40, 11], False),
+    (1, 1, 8192, 1, 1, 128, "bf16", None, False),
+    (2, 1, 33, 8, 1, 128, "bf16", [33, 32], True),
+    (3, 2, 1000, 4, 1, 64, "bf16", [1000, 999, 0], True),
+    (70, 1, 130, 4, 2, 64, "bf16", [130 - i for i in range(70)], True),
+    (1, 7, 517, 2, 2, 128, "bf16", [511], True),
+    (300, 2, 24, 2, 1, 128, "bf16", [i % 25 for i in range(300)], False),
     (1, 1, 1, 1, 1, 32, "f32", None, False),
     (3, 97, 77, 4, 4, 64, "f32", [77, 0, 13], True),
     (2, 64, 65, 6, 2, 128, "f32", [65, 64], False),
@@ -267,7 +273,7 @@ def test_cross_attn_backward(cuda_ok, case):
         assert m > 0 or bool((got["dq"][b] == 0).all())
 
 
-@pytest.mark.parametrize("case", [X[2], X[9], X[15]], ids=str)
+@pytest.mark.parametrize("case", [X[2], X[9], X[-3]], ids=str)
 def test_cross_attn_scale_and_large_scores(cuda_ok, case):
     """A scale of one: scores of tens, weights near one-hot."""
     op, q, k, v, n, clean, dt = x_case(case, 3, scale=1.0)
@@ -276,7 +282,7 @@ def test_cross_attn_scale_and_large_scores(cuda_ok, case):
     x_grads(op, q, k, v, n, clean, dt, 4, 1.0)
 
 
-@pytest.mark.parametrize("case", [X[1], X[9], X[15]], ids=str)
+@pytest.mark.parametrize("case", [X[1], X[9], X[-3]], ids=str)
 def test_cross_attn_rising_scores(cuda_ok, case):
     """Scores that rise along the states: the running maximum moves in every tile."""
     op, q, k, v, n, _, dt = x_case(case, 5, poison=False)
@@ -286,7 +292,7 @@ def test_cross_attn_rising_scores(cuda_ok, case):
     x_forward_check(op, q, k, v, n, dt, op(q, k, v, n))
 
 
-@pytest.mark.parametrize("case", [X[1], X[9], X[15]], ids=str)
+@pytest.mark.parametrize("case", [X[1], X[9], X[-3]], ids=str)
 def test_cross_attn_states_that_weigh_nothing(cuda_ok, case):
     """States with a key of the type's lowest values: scores of -inf or close to it, a weight of zero."""
     op, q, k, v, n, _, dt = x_case(case, 6, poison=False)
@@ -307,7 +313,7 @@ def test_cross_attn_states_that_weigh_nothing(cuda_ok, case):
 
 def test_cross_attn_a_bad_row_stays_alone(cuda_ok):
     """A query row of infinities or NaN gives NaN in its own row only."""
-    for case in (X[9], X[15], X[1]):
+    for case in (X[9], X[-3], X[1]):
         op, q, k, v, n, clean, dt = x_case(case, 7)
         q[0, 0, 1] = math.nan
         q[0, -1, 0, 3] = math.inf
@@ -322,7 +328,7 @@ def test_cross_attn_a_bad_row_stays_alone(cuda_ok):
 
 def test_cross_attn_forward_feeds_backward(cuda_ok):
     """The kept output and log-sum-exp of the kernel's own forward, as a training step uses them."""
-    for case in (X[9], X[3], X[15]):
+    for case in (X[9], X[3], X[-3], X[-9]):
         op, q, k, v, n, (kc, vc), dt = x_case(case, 8)
         y = op(q, k, v, n)
         want, lse, bo = x_forward_check(op, q, kc, vc, n, dt, y)
@@ -340,7 +346,7 @@ def test_cross_attn_gradient_against_differences(cuda_ok):
     """float32: the forward's own central difference along a direction.  With step h the difference has curvature
     terms of h^2 / 6 of the third derivative: h moves a score by at most 0.01 sum_c |k_c| / 8, about 0.06, so they stay
     below 0.06^2 of the gradient times a small number; the forward's errors of 1e-6 over 2 h add less than 1e-3 of it."""
-    op, q, k, v, n, _, dt = x_case(X[15], 10, poison=False)
+    op, q, k, v, n, _, dt = x_case(X[-3], 10, poison=False)
     dy = rnd(gen(11), *q.shape)
     y = op(q, k, v, n)
     got = op.backward(q, k, v, y, op.lse.clone(), dy, n)

@@ -97,6 +97,7 @@ XArgs xargs(const vdn_xattn_args* a, const vdn_xattn_grads* g) {
   return x;
 }
 
+bool few_rows(const vdn_xattn_cfg* c) { return c->dtype == VDN_BF16 && xattn_few_supported(xdims(c, nullptr)); }
 bool on_tensor_cores(const vdn_xattn_cfg* c) { return c->dtype == VDN_BF16 && xattn_tc_supported(xdims(c, nullptr)); }
 
 // --------------------------------------------------------------- 8-bit layer
@@ -147,7 +148,7 @@ vdn_status vdn_qk_norm_rope_bwd(const vdn_qk_cfg* cfg, const vdn_qk_args* args, 
 
 size_t vdn_cross_attn_workspace_size(const vdn_xattn_cfg* cfg) {
   if (check_x(cfg) != VDN_OK) return 0;
-  return kAlign + (on_tensor_cores(cfg) ? up(xattn_tc_scratch(xdims(cfg, nullptr))) : 0);
+  return kAlign + (!few_rows(cfg) && on_tensor_cores(cfg) ? up(xattn_tc_scratch(xdims(cfg, nullptr))) : 0);
 }
 
 size_t vdn_cross_attn_bwd_workspace_size(const vdn_xattn_cfg* cfg) {
@@ -158,8 +159,7 @@ size_t vdn_cross_attn_bwd_workspace_size(const vdn_xattn_cfg* cfg) {
 
 int vdn_cross_attn_impl(const vdn_xattn_cfg* cfg, int backward) {
   if (check_x(cfg) != VDN_OK) return -1;
-  (void)backward;  // both directions alike
-  return on_tensor_cores(cfg) ? 1 : 0;
+  return !backward && few_rows(cfg) ? 2 : on_tensor_cores(cfg) ? 1 : 0;
 }
 
 vdn_status vdn_cross_attn(const vdn_xattn_cfg* cfg, const vdn_xattn_args* args, vdn_stream_t stream) {
@@ -169,6 +169,7 @@ vdn_status vdn_cross_attn(const vdn_xattn_cfg* cfg, const vdn_xattn_args* args, 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const XDims d = xdims(cfg, args);
   const XArgs a = xargs(args, nullptr);
+  if (few_rows(cfg)) return launch_xattn_few(d, a, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
   if (on_tensor_cores(cfg)) return launch_xattn_tc(d, a, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
   return launch_xattn_simt(d, a, cfg->dtype == VDN_BF16, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }

@@ -71,6 +71,10 @@ cudaError_t launch_xattn_simt(const XDims& d, const XArgs& a, bool bf16, cudaStr
 size_t xattn_simt_bwd_scratch(const XDims& d);
 cudaError_t launch_xattn_simt_bwd(const XDims& d, const XArgs& a, bool bf16, cudaStream_t s);
 
+// bf16, d = 64 or 128, up to 8 query rows for a key head (vdn_xattn_few.cu); no scratch
+bool xattn_few_supported(const XDims& d);
+cudaError_t launch_xattn_few(const XDims& d, const XArgs& a, cudaStream_t s);
+
 // bf16 on the tensor cores, d = 64 or 128 (vdn_xattn_tc.cu); scratch: partial results
 bool xattn_tc_supported(const XDims& d);
 size_t xattn_tc_scratch(const XDims& d);
