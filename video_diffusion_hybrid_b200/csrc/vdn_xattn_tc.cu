@@ -16,8 +16,6 @@
 //  - Few items: the key tiles of an item are split over several CTAs, partial
 //    outputs and log-sum-exps go to the workspace in fp32 and a second kernel
 //    joins them in a fixed order.
-//  - A pair with rows for one tile only: both tiles are those rows, and take the
-//    key tiles by turns (even, odd) as two more partial results.
 //
 // Roles (384 threads): warp 0 K producer (TMA, three stages), warp 1 TMEM
 // allocator and MMA issuer, warp 2 V producer (two stages; it zeroes the rows
@@ -62,7 +60,7 @@ __host__ __device__ constexpr uint32_t col_s(int t) { return 256u + 128u * t; }
 struct XtDev {
   int B, Tq, L, H, G;
   int P, TT;           // heads and tokens of a tile (P TT <= 128 rows)
-  int ns, alt;         // splits of the states, tiles alternate over key tiles
+  int ns;              // splits of the states
   ItemGrid grid;       // splits, head groups, tile pairs over the tokens, batch elements: CTAs that run at the
                        // same time share the tokens, and their heads' rows lie side by side in memory
   float scale;
@@ -93,7 +91,7 @@ __device__ __forceinline__ Item decode(const XtDev& x, const ItemPos& p) {
   t.sp = p.d0;
   t.hg = p.d1;
   t.b = p.d3;
-  const int first = p.d2 * (x.alt ? 1 : 2) * x.TT;
+  const int first = p.d2 * 2 * x.TT;
   t.q0 = t.b * x.Tq + first;
   t.left = x.Tq - first;
   const int n = valid_states(x, t.b), all = (n + BN - 1) / BN;
@@ -109,11 +107,7 @@ __device__ __forceinline__ Item decode(const XtDev& x, const ItemPos& p) {
   return t;
 }
 // tile t has rows in this item
-__device__ __forceinline__ bool has_rows(const XtDev& x, const Item& it, int t) { return t == 0 || x.alt || it.left > x.TT; }
-// tile t takes key tile j
-__device__ __forceinline__ bool takes(const XtDev& x, const Item& it, int t, int j) {
-  return x.alt ? (j & 1) == t : has_rows(x, it, t);
-}
+__device__ __forceinline__ bool has_rows(const XtDev& x, const Item& it, int t) { return t == 0 || it.left > x.TT; }
 
 // A CTA's key tiles in order; `n` counts them over all items (its ring position).
 struct Walk {
@@ -140,10 +134,6 @@ struct Walk {
     j = 0;
     pos.next(x.grid);
     settle(x);
-  }
-  // to the next key tile that tile t takes (this one included)
-  __device__ __forceinline__ void seek(const XtDev& x, int t) {
-    while (on && !takes(x, it, t, j)) next(x);
   }
 };
 
@@ -176,6 +166,12 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  // rows past a tile's own are never loaded: zeros, so that nothing a warp does depends on what they hold
+  for (int i = threadIdx.x; i < 2 * NB * (BM - x.P * x.TT) * 8; i += kThr) {
+    const int blk = i / ((BM - x.P * x.TT) * 8), at = i % ((BM - x.P * x.TT) * 8);
+    reinterpret_cast<uint4*>(sQ + blk * BM * 128 + x.P * x.TT * 128)[at] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -235,13 +231,13 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
       const Item it = decode(x, pos);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (!ok || it.nt == 0 || !has_rows(x, it, t) || (x.alt && it.nt <= t)) continue;
+        if (!ok || it.nt == 0 || !has_rows(x, it, t)) continue;
         if (cnt[t] > 0 && !mbar_wait_warp(bar(B_QEMPTY + t), (cnt[t] - 1) & 1, ctl)) { ok = false; continue; }
         if (lane == 0) {
           mbar_expect_tx(bar(B_QFULL + t), bytes);
           for (int c = 0; c < NB; ++c)
             tma_load_3d(smem_u32(sQ + t * QTILE + c * BM * 128), &tmq, bar(B_QFULL + t), c * 64, it.hg * x.P,
-                        it.q0 + (x.alt ? 0 : t * x.TT));
+                        it.q0 + t * x.TT);
         }
         ++cnt[t];
       }
@@ -257,20 +253,16 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
     const uint32_t el = elect_one();
     const uint64_t qd0 = sdesc(smem_u32(sQ), 16, 1024), kd0 = sdesc(smem_u32(sK), 16, 1024);
     const uint64_t vd0 = sdesc(smem_u32(sV), BN * 128, 1024);
-    const int ahead = x.alt ? 2 : 1;
-    Walk nx[2];          // each tile's next scores
-    int nq[2] = {0, 0};  // items begun by each tile
-    int ns[2] = {0, 0}, np[2] = {0, 0};  // key tiles whose scores, and whose O += P V, were issued
-    uint32_t fixes = 0;  // a bit for each stage: parity of its next hand-over by the V producer's zeroing
-    // S_t = Q_t K^T of the tile's next key tile, and the walk moves on
-    auto scores = [&](int t) -> bool {
-      Walk& w = nx[t];
-      const int s = w.n % KST;
-      if (w.j == (x.alt ? t : 0)) {
-        if (!mbar_wait_warp(bar(B_QFULL + t), nq[t] & 1, ctl)) return false;
-        ++nq[t];
+    uint32_t qpar = 0, ppar = 0, fixes = 0;  // parities: of tile t's next Q, its next P, the next zeroed V of a stage
+    Walk w, nx;  // the key tile at hand, the one after it
+    // S_t = Q_t K^T of the key tile n
+    auto scores = [&](int t, const Walk& n) -> bool {
+      const int s = n.n % KST;
+      if (n.j == 0) {
+        if (!mbar_wait_warp(bar(B_QFULL + t), (qpar >> t) & 1, ctl)) return false;
+        qpar ^= 1u << t;
       }
-      if (!mbar_wait_warp(bar(B_KFULL + s), (w.n / KST) & 1, ctl)) return false;
+      if (t == 0 && !mbar_wait_warp(bar(B_KFULL + s), (n.n / KST) & 1, ctl)) return false;
       tc_fence_after();
       const uint64_t qd = dadd(qd0, t * QTILE), kd = dadd(kd0, s * KVBYTES);
       const uint32_t dst = tmem + col_s(t);
@@ -279,58 +271,50 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
         mma_bf16_w(dst, dadd(qd, (k >> 2) * (BM * 128) + (k & 3) * 32), dadd(kd, (k >> 2) * (BN * 128) + (k & 3) * 32), ID_S,
                    k > 0 ? 1u : 0u, el);
       mma_commit_w(bar(B_SFULL + t), el);
-      ++ns[t];
-      if (x.alt || t == 1 || !has_rows(x, w.it, 1)) mma_commit_w(bar(B_KEMPTY + s), el);  // read by every tile that takes it
-      if (w.j + ahead >= w.it.nt) mma_commit_w(bar(B_QEMPTY + t), el);                    // the item's last scores of this tile
-      w.next(x);
-      w.seek(x, t);
+      if (t == 1 || !has_rows(x, n.it, 1)) mma_commit_w(bar(B_KEMPTY + s), el);  // read by both tiles
+      if (n.j + 1 == n.it.nt) mma_commit_w(bar(B_QEMPTY + t), el);               // the item's last scores
       return true;
     };
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      nx[t].start(x);
-      nx[t].seek(x, t);
-    }
-    bool ok = true;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (ok && nx[t].on && nx[t].n < ahead) ok = scores(t);
-    Walk w;
-    for (w.start(x); ok && w.on; w.next(x)) {
+    w.start(x);
+    nx = w;
+    bool ok = true, begun = false;  // the first turn only forms the scores of the first key tile
+#pragma unroll 1
+    while (ok && (w.on || !begun)) {
       const int sv = w.n % VST;
       const bool part = w.it.nk - w.j * BN < BN;
-      bool seen = false;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (ok && takes(x, w.it, t, w.j)) {
-          if (!seen) {  // V of this key tile
+        if (begun && has_rows(x, w.it, t)) {
+          if (t == 0)  // V of this key tile
             ok = mbar_wait_warp(bar(B_VFULL + sv), (w.n / VST) & 1, ctl) &&
                  (!part || mbar_wait_warp(bar(B_VFIX + sv), (fixes >> sv) & 1, ctl));
-            seen = true;
-          }
           // O_t += P_t V in two halves of 64 states, the first one while the softmax forms the second
           const uint64_t vd = dadd(vd0, sv * KVBYTES);
-          const uint32_t dst = tmem + col_o(t), pa = tmem + col_s(t), par = np[t] & 1;
-          const bool first = w.j == (x.alt ? t : 0);
-          ok = ok && mbar_wait_warp(bar(B_PFULL + t), par, ctl);
-          if (!ok) break;
-          tc_fence_after();
+          const uint32_t dst = tmem + col_o(t), pa = tmem + col_s(t);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16_ts_w(dst, pa + 8 * k, dadd(vd, k * 16 * 128), ID_O, (first && k == 0) ? 0u : 1u, el);
-          mma_commit_w(bar(B_OHALF + t), el);
-          ok = mbar_wait_warp(bar(B_PFULL2 + t), par, ctl);
-          if (!ok) break;
-          tc_fence_after();
+          for (int h = 0; h < 2; ++h) {
+            ok = mbar_wait_warp(bar(B_PFULL + 2 * h + t), (ppar >> t) & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-          for (int k = 4; k < 8; ++k) mma_bf16_ts_w(dst, pa + 8 * k, dadd(vd, k * 16 * 128), ID_O, 1u, el);
-          mma_commit_w(bar(B_ODONE + t), el);
-          if (x.alt || t == 1 || !has_rows(x, w.it, 1)) mma_commit_w(bar(B_VEMPTY + sv), el);
-          ++np[t];
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ts_w(dst, pa + 32 * h + 8 * k, dadd(vd, (64 * h + 16 * k) * 128), ID_O, (w.j == 0 && h == 0 && k == 0) ? 0u : 1u, el);
+            mma_commit_w(bar(B_OHALF + 2 * h + t), el);
+          }
+          if (!ok) break;
+          if (t == 1 || !has_rows(x, w.it, 1)) mma_commit_w(bar(B_VEMPTY + sv), el);
+          ppar ^= 1u << t;
         }
-        // the tile's next scores, once its last ones are used up, and no further ahead than the ring reaches
-        if (ok && nx[t].on && ns[t] == np[t] && nx[t].n <= w.n + ahead) ok = scores(t);
+        // the next key tile's scores, over the P that the products above read first
+        if (nx.on && has_rows(x, nx.it, t)) {
+          ok = scores(t, nx);
+          if (!ok) break;
+        }
       }
-      if (part) fixes ^= 1u << sv;
+      if (begun && part) fixes ^= 1u << sv;
+      w = nx;
+      if (nx.on) nx.next(x);
+      begun = true;
     }
     mma_commit_w(bar(B_DRAIN), el);
     mbar_drain(bar(B_DRAIN), 0);
@@ -352,7 +336,7 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
       if (!has_rows(x, it, t)) continue;
       float m_used = -INFINITY, l_sum = 0.f;
       bool any = false;
-      for (int j = x.alt ? t : 0; ok && j < it.nt; j += x.alt ? 2 : 1, ++n) {
+      for (int j = 0; ok && j < it.nt; ++j, ++n) {
         // every TMEM access is warp-collective: control flow stays warp-uniform
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_SFULL + t), n & 1, ctl))) { ok = false; break; }
         tc_fence_after();
@@ -465,8 +449,8 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
       // ---- epilogue: O / l
       if (any && !__all_sync(0xffffffffu, mbar_wait(bar(B_ODONE + t), (n - 1) & 1, ctl))) { ok = false; break; }
       tc_fence_after();
-      const int tok = it.q0 + (x.alt ? 0 : t * x.TT) + rtok;
-      const bool valid = rtok < x.TT && rtok < it.left - (x.alt ? 0 : t * x.TT);
+      const int tok = it.q0 + t * x.TT + rtok;
+      const bool valid = rtok < x.TT && rtok < it.left - t * x.TT;
       const long long gr = (long long)tok * x.H + it.hg * x.P + rhead;
       const float inv = any ? 1.0f / l_sum : 0.f;
       const float lse2 = any ? m_used * c + __log2f(l_sum) : -INFINITY;
@@ -492,7 +476,7 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
           }
         }
       } else {
-        const long long part = x.alt ? 2 * it.sp + t : it.sp, pr = part * x.rows + gr;
+        const long long pr = it.sp * x.rows + gr;
         if (valid) x.pl[pr] = lse2;
         if (any) {
 #pragma unroll 1
@@ -558,7 +542,7 @@ __global__ void __launch_bounds__(256) k_xattn_join(const XtDev x, int parts) {
 constexpr int kSms = 148;
 constexpr int kMaxSplit = 64;
 struct Cut {
-  int P, TT, HG, pairs, ns, alt, parts;
+  int P, TT, HG, pairs, ns, parts;
   long long items;
 };
 Cut cut(const XDims& d) {
@@ -571,20 +555,18 @@ Cut cut(const XDims& d) {
     c.TT = BM / c.P;
     c.HG = d.H / c.P;
     const int nt = (d.L + BN - 1) / BN;
-    c.alt = d.Tq <= c.TT && nt > 1;
-    c.pairs = c.alt ? 1 : (int)(((long long)d.Tq + 2 * c.TT - 1) / (2 * c.TT));
+    c.pairs = (int)(((long long)d.Tq + 2 * c.TT - 1) / (2 * c.TT));
     const long long base = (long long)d.B * c.HG * c.pairs;
     for (int ns = 1; ns <= kMaxSplit && ns <= nt; ++ns) {
       if (ns > 1 && base * ns > 2 * kSms) break;
       const int per = (nt + ns - 1) / ns;
-      const double steps = c.alt ? 0.5 * per + 0.5 : per;
-      const double t = (double)((base * ns + kSms - 1) / kSms) * (steps + 1.5) + (ns > 1 || c.alt ? 2.0 : 0.0);
+      const double t = (double)((base * ns + kSms - 1) / kSms) * (per + 1.5) + (ns > 1 ? 2.0 : 0.0);
       if (best.items == 0 || t < cost) {
         cost = t;
         best = c;
         best.ns = ns;
         best.items = base * ns;
-        best.parts = (ns > 1 || c.alt) ? ns * (c.alt ? 2 : 1) : 0;
+        best.parts = ns > 1 ? ns : 0;
       }
     }
   }
@@ -603,7 +585,7 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   XtDev x{};
   x.B = d.B; x.Tq = d.Tq; x.L = d.L; x.H = d.H; x.G = d.G;
   const unsigned grid = (unsigned)(c.items < kSms ? c.items : kSms);
-  x.P = c.P; x.TT = c.TT; x.ns = c.ns; x.alt = c.alt;
+  x.P = c.P; x.TT = c.TT; x.ns = c.ns;
   x.grid = item_grid((int)c.items, c.ns, c.HG, c.pairs, (int)grid);
   x.scale = d.scale;
   x.kv_len = d.kv_len;
