@@ -30,38 +30,67 @@ __device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162
 __device__ __forceinline__ void st(float* p, float x) { *p = x; }
 __device__ __forceinline__ void st(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+__device__ __forceinline__ float4 ld4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xFFFF0000u));
+}
+
 // Rows [0, n) of src (row stride in elements) to dst[c][r] (transposed, TR) or
-// dst[r][c] (row of D + 4 floats); rows past n as zeros.
+// dst[r][c] (row of D + 4 floats); rows past n as zeros.  Four columns a thread;
+// transposed, neighbours take neighbouring rows (no bank is hit twice, and L1
+// has the rest of a row's sectors for the next turn).
 template <typename T, int D, bool TR>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, long long stride, int n) {
-  for (int i = threadIdx.x; i < BT * D; i += kThr) {
-    const int r = i / D, c = i % D;
-    const float v = r < n ? ld(src + r * stride + c) : 0.f;
-    if (TR) dst[c * PT + r] = v;
-    else dst[r * (D + 4) + c] = v;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < BT * D / 4; i += kThr) {
+    const int r = TR ? i % BT : i / (D / 4), c = 4 * (TR ? i / BT : i % (D / 4));
+    const float4 v = r < n ? ld4(src + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (TR) {
+      dst[c * PT + r] = v.x;
+      dst[(c + 1) * PT + r] = v.y;
+      dst[(c + 2) * PT + r] = v.z;
+      dst[(c + 3) * PT + r] = v.w;
+    } else {
+      *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = v;
+    }
   }
 }
 
-// acc[i][j] += sum_c a[c][ty4 + i] b[c][tx4 + j], both transposed tiles
-template <int D>
-__device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, const float* b, int ty, int tx) {
+// acc[i][j] += sum_c a[c][4 ty + i] b[c][CT tx + j], both transposed tiles: CT columns a thread, 16 CT in all
+template <int D, int CT>
+__device__ __forceinline__ void dot_cols(float (&acc)[4][4], const float* a, const float* b, int ty, int tx) {
 #pragma unroll 4
   for (int c = 0; c < D; ++c) {
     const float4 x = *reinterpret_cast<const float4*>(a + c * PT + 4 * ty);
-    const float4 y = *reinterpret_cast<const float4*>(b + c * PT + 4 * tx);
-    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    float ys[4];
+    if constexpr (CT == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(b + c * PT + 4 * tx);
+      ys[0] = y.x; ys[1] = y.y; ys[2] = y.z; ys[3] = y.w;
+    } else if constexpr (CT == 2) {
+      const float2 y = *reinterpret_cast<const float2*>(b + c * PT + 2 * tx);
+      ys[0] = y.x; ys[1] = y.y;
+    } else {
+      ys[0] = b[c * PT + tx];
+    }
+    const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
+      for (int j = 0; j < CT; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
   }
+}
+template <int D>
+__device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, const float* b, int ty, int tx) {
+  dot_cols<D, 4>(acc, a, b, ty, tx);
 }
 
 // o[i][2 m + e] += sum_j p[j][4 ty + i] v[j][2 (tx + 16 m) + e]: p [column][row] (PT), v [column][D + 4]
 template <int D>
-__device__ __forceinline__ void acc_tile(float (&o)[4][D / 16], const float* p, const float* v, int ty, int tx) {
-#pragma unroll 2
-  for (int j = 0; j < BT; ++j) {
+__device__ __forceinline__ void acc_tile(float (&o)[4][D / 16], const float* p, const float* v, int ty, int tx, int n = BT) {
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
     const float4 x = *reinterpret_cast<const float4*>(p + j * PT + 4 * ty);
     const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -114,6 +143,39 @@ __device__ __forceinline__ void where(long long item, long long per, int heads, 
 template <int D> constexpr size_t fwd_smem() { return sizeof(float) * (2 * D * PT + BT * (D + 4) + BT * PT); }
 template <int D> constexpr size_t bwd_smem() { return sizeof(float) * (4 * D * PT + 2 * BT * (D + 4) + BT * PT); }
 
+// Scores of 64 rows against nk <= 16 CT states, their weights to p[state][row]; running maximum and sum, output rescaled
+template <int D, int CT>
+__device__ __forceinline__ void attend(const float* q, const float* k, float* p, float scale, int nk, int ty, int tx, float (&m)[4],
+                                       float (&l)[4], float (&o)[4][D / 16]) {
+  float s[4][4] = {};
+  dot_cols<D, CT>(s, q, k, ty, tx);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float mx = m[i];
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      s[i][j] = CT * tx + j < nk ? s[i][j] * scale : -INFINITY;
+      mx = fmaxf(mx, s[i][j]);
+    }
+    mx = half_max(mx);
+    // a row whose scores are all -inf so far keeps its reference at zero: no inf - inf
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float f = expf(m[i] - ref);
+    m[i] = mx;
+    l[i] *= f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) o[i][j] *= f;
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      s[i][j] = expf(s[i][j] - ref);
+      l[i] += s[i][j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < CT; ++j)
+    *reinterpret_cast<float4*>(p + (CT * tx + j) * PT + 4 * ty) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThr) k_xattn(const XDims d, const XArgs a) {
   clear_status(a.status);
@@ -141,33 +203,12 @@ __global__ void __launch_bounds__(kThr) k_xattn(const XDims d, const XArgs a) {
     load_tile<T, D, true>(sK, k + k0 * d.ks, d.ks, nk);
     load_tile<T, D, false>(sV, v + k0 * d.vs, d.vs, nk);
     __syncthreads();
-    float s[4][4] = {};
-    dot_tile<D>(s, sQ, sK, ty, tx);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float mx = m[i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = 4 * tx + j < nk ? s[i][j] * d.scale : -INFINITY;
-        mx = fmaxf(mx, s[i][j]);
-      }
-      mx = half_max(mx);
-      // a row whose scores are all -inf so far keeps its reference at zero: no inf - inf
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      const float f = expf(m[i] - ref);
-      m[i] = mx;
-      l[i] *= f;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) o[i][j] *= f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = expf(s[i][j] - ref);
-        l[i] += p;
-        sP[(4 * tx + j) * PT + 4 * ty + i] = p;
-      }
-    }
+    // a tile's columns: four a thread, or two or one where no more states are left
+    if (nk > 32) attend<D, 4>(sQ, sK, sP, d.scale, nk, ty, tx, m, l, o);
+    else if (nk > 16) attend<D, 2>(sQ, sK, sP, d.scale, nk, ty, tx, m, l, o);
+    else attend<D, 1>(sQ, sK, sP, d.scale, nk, ty, tx, m, l, o);
     __syncthreads();
-    acc_tile<D>(o, sP, sV, ty, tx);
+    acc_tile<D>(o, sP, sV, ty, tx, nk);
   }
   float inv[4];
 #pragma unroll
