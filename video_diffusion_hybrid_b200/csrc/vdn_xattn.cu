@@ -13,7 +13,7 @@
 // A block of 256 threads has 64 rows against tiles of 64 columns; a thread has
 // a 4 x 4 piece of the score tile and 4 x D/16 of the product behind it, fed
 // by 16-byte shared-memory reads of transposed operands.  Bound by the fp32
-// pipe and those reads; one launch (the backward: three) without atomics.
+// pipe and those reads; one launch (the backward: three, or four) without atomics.
 #include <cuda_bf16.h>
 
 #include "vdn_xattn.h"
@@ -282,16 +282,24 @@ __global__ void __launch_bounds__(kThr) k_xattn_dq(const XDims d, const XArgs a,
   store_rows<T, D>(static_cast<T*>(a.dq) + qrow * D, (long long)d.H * D, nq, o, f, ty, tx);
 }
 
-// dk and dv of 64 states of one key head, over its G query heads and all query rows
+// Splits of the dk / dv sums over the group's query tiles, so that there is about a CTA for every SM (they take one
+// each): partial sums [ns][B L Hkv][D] in fp32, joined in order.
+struct KvSplit {
+  int ns, per;       // splits, query tiles of each (over the G heads of a group, tile fastest)
+  float *dk, *dv;    // partial sums, null with one split
+};
+
+// dk and dv of 64 states of one key head, over its G query heads and all query rows (or a split's share of them)
 template <typename T, int D>
-__global__ void __launch_bounds__(kThr) k_xattn_dkv(const XDims d, const XArgs a, const float* delta) {
+__global__ void __launch_bounds__(kThr) k_xattn_dkv(const XDims d, const XArgs a, const float* delta, const KvSplit sp) {
   extern __shared__ __align__(16) float sm[];
   float *sK = sm, *sV = sK + D * PT, *sQ = sV + D * PT, *sDO = sQ + D * PT, *sQr = sDO + D * PT, *sDOr = sQr + BT * (D + 4),
         *sP = sDOr + BT * (D + 4);  // P, then dS: one buffer (D = 128 has no room for two)
   __shared__ float sL[BT], sD[BT];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   int b, hk, k0;
-  where(blockIdx.x, (d.L + BT - 1) / BT, d.Hkv, b, hk, k0);
+  where(blockIdx.x / sp.ns, (d.L + BT - 1) / BT, d.Hkv, b, hk, k0);
+  const int split = blockIdx.x % sp.ns, nqt = (d.Tq + BT - 1) / BT, u0 = split * sp.per, u1 = min(u0 + sp.per, d.G * nqt);
   const int rows = min(BT, d.L - k0), nk = max(0, min(rows, kv_valid(d, b) - k0));
   const T* k = static_cast<const T*>(a.k) + ((long long)b * d.L + k0) * d.ks + (long long)hk * D;
   const T* v = static_cast<const T*>(a.v) + ((long long)b * d.L + k0) * d.vs + (long long)hk * D;
@@ -302,9 +310,9 @@ __global__ void __launch_bounds__(kThr) k_xattn_dkv(const XDims d, const XArgs a
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) ok[i][j] = ov[i][j] = 0.f;
-  for (int g = 0; g < d.G && nk > 0; ++g)
-    for (int q0 = 0; q0 < d.Tq; q0 += BT) {
-      const int nq = min(BT, d.Tq - q0);
+  if (nk > 0)
+    for (int u = u0; u < u1; ++u) {
+      const int g = u / nqt, q0 = u % nqt * BT, nq = min(BT, d.Tq - q0);
       const long long qrow = ((long long)b * d.Tq + q0) * d.H + hk * d.G + g;
       const T *q = static_cast<const T*>(a.q) + qrow * D, *dy = static_cast<const T*>(a.dy) + qrow * D;
       __syncthreads();
@@ -342,9 +350,40 @@ __global__ void __launch_bounds__(kThr) k_xattn_dkv(const XDims d, const XArgs a
     }
   const float fk[4] = {d.scale, d.scale, d.scale, d.scale}, fv[4] = {1.f, 1.f, 1.f, 1.f};
   const long long krow = ((long long)b * d.L + k0) * d.Hkv + hk;
+  if (sp.dk != nullptr) {
+    const long long at = (split * (long long)d.B * d.L * d.Hkv + krow) * D;
+    store_rows<float, D>(sp.dk + at, (long long)d.Hkv * D, rows, ok, fk, ty, tx);
+    store_rows<float, D>(sp.dv + at, (long long)d.Hkv * D, rows, ov, fv, ty, tx);
+    return;
+  }
   store_rows<T, D>(static_cast<T*>(a.dk) + krow * D, (long long)d.Hkv * D, rows, ok, fk, ty, tx);
   store_rows<T, D>(static_cast<T*>(a.dv) + krow * D, (long long)d.Hkv * D, rows, ov, fv, ty, tx);
 }
+
+// the splits' sums in order, an element of dk and one of dv a thread
+template <typename T>
+__global__ void __launch_bounds__(256) k_xattn_join(const KvSplit sp, T* dk, T* dv, long long n) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float k = 0.f, v = 0.f;
+  for (int s = 0; s < sp.ns; ++s) {
+    k += sp.dk[s * n + i];
+    v += sp.dv[s * n + i];
+  }
+  st(dk + i, k);
+  st(dv + i, v);
+}
+
+KvSplit kv_split(const XDims& d) {
+  const long long items = (long long)d.B * d.Hkv * ((d.L + BT - 1) / BT), all = (long long)d.G * ((d.Tq + BT - 1) / BT);
+  long long ns = items < 148 ? 148 / items : 1;
+  if (ns > all) ns = all;
+  KvSplit s{};
+  s.per = (int)((all + ns - 1) / ns);
+  s.ns = (int)((all + s.per - 1) / s.per);
+  return s;
+}
+size_t delta_bytes(const XDims& d) { return ((size_t)d.B * d.Tq * d.H * sizeof(float) + 255) / 256 * 256; }
 
 template <typename K>
 bool grow_smem(K kern, size_t bytes) {
@@ -370,13 +409,24 @@ cudaError_t bwd(const XDims& d, const XArgs& a, cudaStream_t s) {
   const long long qi = (long long)d.B * d.H * ((d.Tq + BT - 1) / BT), ki = (long long)d.B * d.Hkv * ((d.L + BT - 1) / BT);
   k_xattn_dq<T, D><<<(unsigned)qi, kThr, bwd_smem<D>(), s>>>(d, a, delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_xattn_dkv<T, D><<<(unsigned)ki, kThr, bwd_smem<D>(), s>>>(d, a, delta);
+  KvSplit sp = kv_split(d);
+  const long long n = (long long)d.B * d.L * d.Hkv * D;
+  if (sp.ns > 1) {
+    sp.dk = reinterpret_cast<float*>(static_cast<char*>(a.scratch) + delta_bytes(d));
+    sp.dv = sp.dk + sp.ns * n;
+  }
+  k_xattn_dkv<T, D><<<(unsigned)(ki * sp.ns), kThr, bwd_smem<D>(), s>>>(d, a, delta, sp);
+  if ((e = cudaGetLastError()) != cudaSuccess || sp.ns == 1) return e;
+  k_xattn_join<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(sp, static_cast<T*>(a.dk), static_cast<T*>(a.dv), n);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t xattn_simt_bwd_scratch(const XDims& d) { return (size_t)d.B * d.Tq * d.H * sizeof(float); }
+size_t xattn_simt_bwd_scratch(const XDims& d) {
+  const KvSplit s = kv_split(d);
+  return delta_bytes(d) + (s.ns > 1 ? 2 * (size_t)s.ns * d.B * d.L * d.Hkv * d.d * sizeof(float) : 0);
+}
 
 cudaError_t launch_xattn_simt(const XDims& d, const XArgs& a, bool bf16, cudaStream_t s) {
   switch (d.d) {
