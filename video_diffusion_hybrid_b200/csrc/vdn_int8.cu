@@ -182,11 +182,20 @@ cudaError_t quantize(const T* x, int rows, int cols, uint2* q, float* scale, uin
 // Up to kFewRows rows: the product is bound by the read of the weight, once.
 // Every block forms the codes of all rows in shared memory by itself (x is
 // small and stays in L2), which saves a launch; a warp has NC output channels
-// and walks K in steps of 512 bytes, four byte products per instruction.
+// and walks K in steps of 512 bytes, four byte products per instruction.  Its
+// first AHEAD steps of the weight are under way while the codes are formed.
 constexpr int kFewRows = 8;
 constexpr int NC = 2;           // channels per warp
+constexpr int AHEAD = 8;        // steps
 constexpr int kFewThreads = 256;
 constexpr size_t kFewSmem = 200 * 1024;
+
+// a read-only load that stays where it is written, ahead of the work that hides it
+__device__ __forceinline__ uint4 load_pinned(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 template <typename T, typename To, int MR>
 __global__ void __launch_bounds__(kFewThreads) k_int8_few(int M, int K, int N, const void* __restrict__ xp,
@@ -198,34 +207,45 @@ __global__ void __launch_bounds__(kFewThreads) k_int8_few(int M, int K, int N, c
   __shared__ float sx[MR];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nv = K / 16;
   const int n0 = (blockIdx.x * (kFewThreads / 32) + warp) * NC;
-  // rows' codes and scales
-  for (int m = 0; m < M; ++m) {
-    unsigned char* dst = sm + (size_t)m * K;
-    if (x_scale != nullptr) {
-      const uint4* src = static_cast<const uint4*>(xp) + (size_t)m * nv;
-      for (int i = threadIdx.x; i < nv; i += kFewThreads) reinterpret_cast<uint4*>(dst)[i] = __ldg(src + i);
-      if (threadIdx.x == 0) sx[m] = __ldg(x_scale + m);
-    } else {
-      const T* src = static_cast<const T*>(xp) + (size_t)m * K;
-      uint32_t mx = 0;
-      for (int i = threadIdx.x; i < K / 8; i += kFewThreads) {
-        float v[8];
-        load8(src + 8 * i, v);
-        mx = max(mx, abs_bits(v));
-      }
-      mx = __reduce_max_sync(0xffffffffu, mx);
+  const uint4* wr = w + (size_t)n0 * nv;  // N is a multiple of NC
+  uint4 first[AHEAD][NC];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      first[i][j] = make_uint4(0, 0, 0, 0);
+      if (n0 < N && lane + 32 * i < nv) first[i][j] = load_pinned(wr + (size_t)j * nv + lane + 32 * i);
+    }
+  // rows' codes and scales: one row by the whole block, several by a warp each (M <= 8 = the warps)
+  if (x_scale != nullptr) {
+    for (int i = threadIdx.x; i < M * nv; i += kFewThreads) reinterpret_cast<uint4*>(sm)[i] = __ldg(static_cast<const uint4*>(xp) + i);
+    if (threadIdx.x < M) sx[threadIdx.x] = __ldg(x_scale + threadIdx.x);
+  } else if (MR == 1 || warp < M) {
+    const int m = MR == 1 ? 0 : warp, t0 = MR == 1 ? threadIdx.x : lane;
+    constexpr int TS = MR == 1 ? kFewThreads : 32;
+    const T* src = static_cast<const T*>(xp) + (size_t)m * K;
+    uint32_t mx = 0;
+#pragma unroll 4
+    for (int i = t0; i < K / 8; i += TS) {
+      float v[8];
+      load8(src + 8 * i, v);
+      mx = max(mx, abs_bits(v));
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (MR == 1) {
       if (lane == 0) red[warp] = mx;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kFewThreads / 32; ++i) mx = max(mx, red[i]);
-      __syncthreads();
-      const Scale c = scale_of(mx);
-      if (threadIdx.x == 0) sx[m] = c.s;
-      for (int i = threadIdx.x; i < K / 8; i += kFewThreads) {
-        float v[8];
-        load8(src + 8 * i, v);
-        reinterpret_cast<uint2*>(dst)[i] = codes8(v, c);
-      }
+    }
+    const Scale c = scale_of(mx);
+    if (t0 == 0) sx[m] = c.s;
+    uint2* dst = reinterpret_cast<uint2*>(sm + (size_t)m * K);
+#pragma unroll 4
+    for (int i = t0; i < K / 8; i += TS) {
+      float v[8];
+      load8(src + 8 * i, v);
+      dst[i] = codes8(v, c);
     }
   }
   __syncthreads();
@@ -235,12 +255,7 @@ __global__ void __launch_bounds__(kFewThreads) k_int8_few(int M, int K, int N, c
   for (int m = 0; m < MR; ++m)
 #pragma unroll
     for (int j = 0; j < NC; ++j) acc[m][j] = 0;
-  const uint4* wr = w + (size_t)n0 * nv;  // N is a multiple of NC
-#pragma unroll 4
-  for (int i = lane; i < nv; i += 32) {
-    uint4 u[NC];
-#pragma unroll
-    for (int j = 0; j < NC; ++j) u[j] = __ldg(wr + (size_t)j * nv + i);
+  auto step = [&](const uint4 (&u)[NC], int i) {
 #pragma unroll
     for (int m = 0; m < MR; ++m) {
       if (m >= M) continue;
@@ -253,6 +268,16 @@ __global__ void __launch_bounds__(kFewThreads) k_int8_few(int M, int K, int N, c
         acc[m][j] = __dp4a((int)a.w, (int)u[j].w, acc[m][j]);
       }
     }
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (lane + 32 * i < nv) step(first[i], lane + 32 * i);
+#pragma unroll 4
+  for (int i = lane + 32 * AHEAD; i < nv; i += 32) {
+    uint4 u[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) u[j] = __ldg(wr + (size_t)j * nv + i);
+    step(u, i);
   }
 #pragma unroll
   for (int m = 0; m < MR; ++m) {
