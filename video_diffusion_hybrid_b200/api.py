@@ -255,11 +255,14 @@ class _Streamed:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._like = torch.empty(0, device=self.device)
 
-    def _call(self, fn, *args, stream=None):
-        if torch.cuda.current_device() == self.device.index:
-            return fn(*args, stream)
-        with torch.cuda.device(self.device):
-            return fn(*args, stream)
+    def _call(self, name, stream, *args):
+        """The library's function with the operator's device current, on `stream` or that device's current one."""
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._call(name, stream, *args)
+        st = getattr(L.lib(), name)(*args, L._stream_handle(stream))
+        if st != L.VDN_OK:
+            raise L.VdnError(st, name)
 
     def _new(self, shape, dtype, stream=None) -> torch.Tensor:
         """A tensor that belongs to the stream of the call: its memory is not
@@ -295,9 +298,10 @@ class QKNormRope(_Streamed):
             raise L.VdnError(L.VDN_ERR_INVALID_ARG, "QKNormRope")
         self.axes, self.pairing, self.eps = len(self.sections), pair[pairing], eps
         self.c_sections = (ctypes.c_int * 3)(*self.sections)
+        self._cfgs = {}  # by sizes and strides
         self.wq_shape, self.wk_shape = ((Hq, d), (Hk, d)) if per_head else ((d,), (d,))
 
-    def _cfg_args(self, q, k, wq, wk, table, pos):
+    def _cfg_args(self, q, k, wq, wk, table, pos, grad=0):
         lead, dt, dev = q.shape[:-2], q.dtype, self.device
         qs = _head_rows(q, "q", lead, self.Hq, self.d, dt, dev)
         ks = _head_rows(k, "k", lead, self.Hk, self.d, dt, dev) if self.Hk else 0
@@ -312,8 +316,11 @@ class QKNormRope(_Streamed):
         if pos is not None:
             _need(pos, "pos", lead if self.axes == 1 and pos.dim() == len(lead) else (*lead, self.axes), torch.int32, dev)
             rows = rows or 2**31 - 1
-        cfg = L.QkCfg(math.prod(lead), self.Hq, self.Hk, self.d, self.rot, self.pairing, self.axes, self.c_sections, rows,
-                      int(self.per_head), _dtype_of(q), 0, self.eps, qs, ks)
+        key = (lead, rows, dt, grad, qs, ks)
+        cfg = self._cfgs.get(key)
+        if cfg is None:
+            cfg = self._cfgs[key] = L.QkCfg(math.prod(lead), self.Hq, self.Hk, self.d, self.rot, self.pairing, self.axes,
+                                            self.c_sections, rows, int(self.per_head), _dtype_of(q), grad, self.eps, qs, ks)
         return cfg, L.QkArgs(q.data_ptr(), k.data_ptr() if self.Hk else None, L._ptr(wq), L._ptr(wk),
                              table.data_ptr() if self.rot else None, L._ptr(pos))
 
@@ -326,14 +333,13 @@ class QKNormRope(_Streamed):
             _need(out[0], "q_out", q.shape, q.dtype, self.device)
             _need(out[1], "k_out", k.shape if self.Hk else (), q.dtype, self.device)
         args.q_out, args.k_out = out[0].data_ptr(), L._ptr(out[1])
-        self._call(L.vdn_qk_norm_rope, cfg, args, stream=stream)
+        self._call("vdn_qk_norm_rope", stream, cfg, args)
         return out
 
     def backward(self, q, k, wq, wk, table, dq_out, dk_out, pos=None, stream=None) -> dict:
         """dq, dk (q's type) and dwq, dwk (float32) from the gradients of the
         outputs (float32, or q's type)."""
-        cfg, args = self._cfg_args(q, k, wq, wk, table, pos)
-        cfg.grad_dtype = _dtype_of(dq_out)
+        cfg, args = self._cfg_args(q, k, wq, wk, table, pos, _dtype_of(dq_out))
         _need(dq_out, "dq_out", q.shape, dq_out.dtype, self.device)
         if self.Hk:
             _need(dk_out, "dk_out", k.shape, dq_out.dtype, self.device)
@@ -344,7 +350,7 @@ class QKNormRope(_Streamed):
             g["dk"], g["dwk"] = new(k.shape, q.dtype), new(self.wk_shape, torch.float32)
         gr = L.QkGrads(L._ptr(dq_out), L._ptr(dk_out) if self.Hk else None, L._ptr(g["dq"]), L._ptr(g.get("dk")),
                        L._ptr(g["dwq"]), L._ptr(g.get("dwk")), ws.data_ptr(), ws.numel())
-        self._call(L.vdn_qk_norm_rope_bwd, cfg, args, gr, stream=stream)
+        self._call("vdn_qk_norm_rope_bwd", stream, cfg, args, gr)
         return g
 
 
@@ -369,7 +375,9 @@ class CrossAttention(_Streamed):
         super().__init__(device)
         self.shape, self.kv_shape = (B, Tq, H, d), (B, L_, Hkv, d)
         self.torch_dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
-        self.cfg = L.XattnCfg(B=B, Tq=Tq, L=L_, H=H, Hkv=Hkv, d=d, dtype=L.VDN_BF16 if dtype == "bf16" else L.VDN_F32, scale=scale)
+        self.sizes = (B, Tq, L_, H, Hkv, d, L.VDN_BF16 if dtype == "bf16" else L.VDN_F32, scale)
+        self.cfg = L.XattnCfg(*self.sizes)
+        self._cfgs = {}  # by the strides of k and v
         self.need, self.bwd_need = L.vdn_cross_attn_workspace_size(self.cfg), L.vdn_cross_attn_bwd_workspace_size(self.cfg)
         if self.need == 0:
             raise L.VdnError(L.VDN_ERR_INVALID_ARG, "vdn_cross_attn_workspace_size")
@@ -381,41 +389,43 @@ class CrossAttention(_Streamed):
         B, _, Hkv, d = self.kv_shape
         _need(q, "q", self.shape, self.torch_dtype, self.device)
         _need(kv_len, "kv_len", (B,), torch.int32, self.device)
-        self.cfg.k_stride = _head_rows(k, "k", self.kv_shape[:2], Hkv, d, self.torch_dtype, self.device)
-        self.cfg.v_stride = _head_rows(v, "v", self.kv_shape[:2], Hkv, d, self.torch_dtype, self.device)
-        return L.XattnArgs(q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), kv_len=L._ptr(kv_len))
+        key = (_head_rows(k, "k", self.kv_shape[:2], Hkv, d, self.torch_dtype, self.device),
+               _head_rows(v, "v", self.kv_shape[:2], Hkv, d, self.torch_dtype, self.device))
+        cfg = self._cfgs.get(key)
+        if cfg is None:
+            cfg = self._cfgs[key] = L.XattnCfg(*self.sizes, *key)
+        return cfg, L.XattnArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), L._ptr(kv_len))
 
     def __call__(self, q, k, v, kv_len=None, out=None, stream=None) -> torch.Tensor:
-        a = self._inputs(q, k, v, kv_len)
+        cfg, a = self._inputs(q, k, v, kv_len)
         if out is None:
             out = self._new(self.shape, self.torch_dtype, stream)
         else:
             _need(out, "out", self.shape, self.torch_dtype, self.device)
-        self.workspace = self._new(self.need, torch.uint8, stream)
-        a.y, a.lse = out.data_ptr(), L._ptr(self.lse)
-        a.workspace, a.workspace_bytes = self.workspace.data_ptr(), self.workspace.numel()
-        self._call(L.vdn_cross_attn, self.cfg, a, stream=stream)
+        self.workspace = ws = self._new(self.need, torch.uint8, stream)
+        a.y, a.lse, a.workspace, a.workspace_bytes = out.data_ptr(), L._ptr(self.lse), ws.data_ptr(), self.need
+        self._call("vdn_cross_attn", stream, cfg, a)
         return out
 
     def backward(self, q, k, v, y, lse, dy, kv_len=None, stream=None) -> dict:
         """dq, dk, dv from the forward's output y and log-sum-exp."""
-        a = self._inputs(q, k, v, kv_len)
+        cfg, a = self._inputs(q, k, v, kv_len)
         _need(y, "y", self.shape, self.torch_dtype, self.device)
         _need(dy, "dy", self.shape, self.torch_dtype, self.device)
         _need(lse, "lse", self.shape[:3], torch.float32, self.device)
-        self.bwd_workspace = self._new(self.bwd_need, torch.uint8, stream)
-        a.y, a.lse = y.data_ptr(), lse.data_ptr()
-        a.workspace, a.workspace_bytes = self.bwd_workspace.data_ptr(), self.bwd_workspace.numel()
+        self.bwd_workspace = ws = self._new(self.bwd_need, torch.uint8, stream)
+        a.y, a.lse, a.workspace, a.workspace_bytes = y.data_ptr(), lse.data_ptr(), ws.data_ptr(), self.bwd_need
         new = lambda shape: self._new(shape, self.torch_dtype, stream)  # noqa: E731
         g = {"dq": new(self.shape), "dk": new(self.kv_shape), "dv": new(self.kv_shape)}
         gr = L.XattnGrads(dy.data_ptr(), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr())
-        self._call(L.vdn_cross_attn_bwd, self.cfg, a, gr, stream=stream)
+        self._call("vdn_cross_attn_bwd", stream, cfg, a, gr)
         return g
 
     def status(self, backward: bool = False, stream=None) -> tuple:
         """(status, kernel tag) of the last forward (or backward) call's bounded waits."""
         ws = self.bwd_workspace if backward else self.workspace
-        return self._call(L.vdn_cross_attn_device_status, ws, stream=stream)
+        with torch.cuda.device(self.device):
+            return L.vdn_cross_attn_device_status(ws, stream)
 
 
 def quantize_int8(x: torch.Tensor, stream=None) -> tuple:
@@ -425,7 +435,7 @@ def quantize_int8(x: torch.Tensor, stream=None) -> tuple:
         raise ValueError("quantize_int8: expected a contiguous matrix")
     on = _Streamed(x.device)
     q, scale = on._new(x.shape, torch.int8, stream), on._new(x.shape[:1], torch.float32, stream)
-    on._call(L.vdn_quantize_int8, x, _dtype_of(x), x.shape[0], x.shape[1], q, scale, stream=stream)
+    on._call("vdn_quantize_int8", stream, x.data_ptr(), _dtype_of(x), x.shape[0], x.shape[1], q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -443,6 +453,7 @@ class Int8Linear(_Streamed):
         _need(w_scale, "w_scale", (self.N,), torch.float32, self.device)
         _need(bias, "bias", (self.N,), torch.float32, self.device)
         self.w, self.w_scale, self.bias = w, w_scale, bias
+        self._cfgs = {}  # configuration and workspace size by rows and type
         self.out_torch = {"bf16": torch.bfloat16, "f32": torch.float32}[out_dtype]
         self.out_dtype = L.VDN_BF16 if out_dtype == "bf16" else L.VDN_F32
 
@@ -452,8 +463,11 @@ class Int8Linear(_Streamed):
             raise ValueError(f"Int8Linear: expected a contiguous [..., {self.K}] tensor on {self.device}")
         M = x.numel() // self.K
         _need(x_scale, "x_scale", x.shape[:-1], torch.float32, self.device)
-        cfg = L.Int8Cfg(M=M, K=self.K, N=self.N, x_dtype=L.VDN_I8 if codes else _dtype_of(x), out_dtype=self.out_dtype)
-        need = L.vdn_linear_int8_workspace_size(cfg)
+        found = self._cfgs.get((M, x.dtype))
+        if found is None:
+            cfg = L.Int8Cfg(M, self.K, self.N, L.VDN_I8 if codes else _dtype_of(x), self.out_dtype)
+            found = self._cfgs[M, x.dtype] = cfg, L.vdn_linear_int8_workspace_size(cfg)
+        cfg, need = found
         ws = self._new(need, torch.uint8, stream) if need else None
         shape = (*x.shape[:-1], self.N)
         if out is None:
@@ -462,5 +476,5 @@ class Int8Linear(_Streamed):
             _need(out, "out", shape, self.out_torch, self.device)
         a = L.Int8Args(x.data_ptr(), L._ptr(x_scale), self.w.data_ptr(), self.w_scale.data_ptr(), L._ptr(self.bias),
                        out.data_ptr(), L._ptr(ws), need)
-        self._call(L.vdn_linear_int8, cfg, a, stream=stream)
+        self._call("vdn_linear_int8", stream, cfg, a)
         return out

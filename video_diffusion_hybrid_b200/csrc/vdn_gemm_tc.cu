@@ -394,9 +394,8 @@ vdn_status launch_small(int M, int K, int N, const void* a, const void* w, void*
   g.tiles = g.tiles_n * ((M + TM - 1) / TM);
   g.nkb = (K + KBYTES - 1) / KBYTES;
   g.out = out;
-  auto kern = k_gemm_s8_small<TNS, To>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)small_smem<TNS>()) != cudaSuccess) return VDN_ERR_CUDA;
-  kern<<<g.tiles, kThreadsG, small_smem<TNS>(), s>>>(g, ma, mb);
+  if (allow_smem<k_gemm_s8_small<TNS, To>>(small_smem<TNS>()) != cudaSuccess) return VDN_ERR_CUDA;
+  k_gemm_s8_small<TNS, To><<<g.tiles, kThreadsG, small_smem<TNS>(), s>>>(g, ma, mb);
   return cudaGetLastError() == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
 
@@ -480,8 +479,15 @@ vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const floa
 }
 
 uint32_t* status_of_proj() {
-  void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_proj_status) != cudaSuccess) return nullptr;
+  // the symbol's address on each device, looked up once
+  static std::atomic<void*> at[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  void* p = dev < 64 ? at[dev].load(std::memory_order_relaxed) : nullptr;
+  if (p == nullptr) {
+    if (cudaGetSymbolAddress(&p, g_proj_status) != cudaSuccess) return nullptr;
+    if (dev < 64) at[dev].store(p, std::memory_order_relaxed);
+  }
   return static_cast<uint32_t*>(p);
 }
 

@@ -298,7 +298,7 @@ template <typename T, typename To, int MR>
 cudaError_t few(const vdn_int8_cfg& c, const vdn_int8_args& a, cudaStream_t s) {
   auto kern = k_int8_few<T, To, MR>;
   const size_t smem = (size_t)c.M * c.K;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+  const cudaError_t e = allow_smem<k_int8_few<T, To, MR>>(kFewSmem);
   if (e != cudaSuccess) return e;
   const int per = kFewThreads / 32 * NC;
   kern<<<(c.N + per - 1) / per, kFewThreads, smem, s>>>(c.M, c.K, c.N, a.x, c.x_dtype == VDN_I8 ? a.x_scale : nullptr,

@@ -520,22 +520,22 @@ QkDev device_args(const vdn_qk_cfg& c, const vdn_qk_args& in) {
   return a;
 }
 
-template <typename K>
-cudaError_t go(K kern, const QkDev& a, size_t smem, unsigned grid, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <auto Kernel>
+cudaError_t go(const QkDev& a, size_t smem, unsigned grid, cudaStream_t s) {
+  const cudaError_t e = allow_smem<Kernel>(smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, a.threads, smem, s>>>(a);
+  Kernel<<<grid, a.threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <typename T, int LPR, int HU>
 cudaError_t go_fwd(const QkDev& a, bool split, unsigned grid, cudaStream_t s) {
-  return split ? go(k_qk_fwd<T, LPR, true, HU>, a, fwd_smem<T, HU>(), grid, s)
-               : go(k_qk_fwd<T, LPR, false, HU>, a, fwd_smem<T, HU>(), grid, s);
+  return split ? go<k_qk_fwd<T, LPR, true, HU>>(a, fwd_smem<T, HU>(), grid, s)
+               : go<k_qk_fwd<T, LPR, false, HU>>(a, fwd_smem<T, HU>(), grid, s);
 }
 template <typename T, typename G, int LPR, int HU>
 cudaError_t go_bwd(const QkDev& a, bool split, unsigned grid, cudaStream_t s) {
-  return split ? go(k_qk_bwd<T, G, LPR, true, HU>, a, bwd_smem<T, G, HU>(), grid, s)
-               : go(k_qk_bwd<T, G, LPR, false, HU>, a, bwd_smem<T, G, HU>(), grid, s);
+  return split ? go<k_qk_bwd<T, G, LPR, true, HU>>(a, bwd_smem<T, G, HU>(), grid, s)
+               : go<k_qk_bwd<T, G, LPR, false, HU>>(a, bwd_smem<T, G, HU>(), grid, s);
 }
 template <typename T, int LPR>
 cudaError_t run_fwd(const QkDev& a, bool split, int hu, unsigned grid, cudaStream_t s) {

@@ -385,15 +385,11 @@ KvSplit kv_split(const XDims& d) {
 }
 size_t delta_bytes(const XDims& d) { return ((size_t)d.B * d.Tq * d.H * sizeof(float) + 255) / 256 * 256; }
 
-template <typename K>
-bool grow_smem(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-}
-
 template <typename T, int D>
 cudaError_t fwd(const XDims& d, const XArgs& a, cudaStream_t s) {
   const long long items = (long long)d.B * d.H * ((d.Tq + BT - 1) / BT);
-  if (!grow_smem(k_xattn<T, D>, fwd_smem<D>())) return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem<k_xattn<T, D>>(fwd_smem<D>());
+  if (e != cudaSuccess) return e;
   k_xattn<T, D><<<(unsigned)items, kThr, fwd_smem<D>(), s>>>(d, a);
   return cudaGetLastError();
 }
@@ -405,7 +401,8 @@ cudaError_t bwd(const XDims& d, const XArgs& a, cudaStream_t s) {
   k_xattn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(static_cast<const T*>(a.y), static_cast<const T*>(a.dy), delta, rows, D, a.status);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (!grow_smem(k_xattn_dq<T, D>, bwd_smem<D>()) || !grow_smem(k_xattn_dkv<T, D>, bwd_smem<D>())) return cudaErrorInvalidValue;
+  if ((e = allow_smem<k_xattn_dq<T, D>>(bwd_smem<D>())) != cudaSuccess || (e = allow_smem<k_xattn_dkv<T, D>>(bwd_smem<D>())) != cudaSuccess)
+    return e;
   const long long qi = (long long)d.B * d.H * ((d.Tq + BT - 1) / BT), ki = (long long)d.B * d.Hkv * ((d.L + BT - 1) / BT);
   k_xattn_dq<T, D><<<(unsigned)qi, kThr, bwd_smem<D>(), s>>>(d, a, delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -914,9 +914,9 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   const long long qi = (long long)d.B * d.H * c.nqt * c.qs, ki = (long long)d.B * d.Hkv * c.nkt * c.ks;
   if (qi > 0x7FFFFFFFLL || ki > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const size_t smq = 1024 + (size_t)7 * BR * D * 2 + BR * sizeof(float2) + 32 * 8 + 16, smk = dkv_smem<D>();
-  cudaError_t e = cudaFuncSetAttribute(k_xattn_dq_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smq);
+  cudaError_t e = allow_smem<k_xattn_dq_tc<D>>(smq);
   if (e != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(k_xattn_dkv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smk)) != cudaSuccess) return e;
+  if ((e = allow_smem<k_xattn_dkv_tc<D>>(smk)) != cudaSuccess) return e;
   const long long rows = (long long)d.B * d.Tq * d.H, per = 256 / (D / 8) * 4;
   k_xattn_delta_bf16<D><<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(x, rows);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

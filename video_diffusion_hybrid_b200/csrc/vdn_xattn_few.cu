@@ -273,7 +273,8 @@ cudaError_t launch(const XfDev& x, int warps, unsigned grid, cudaStream_t s) {
   const size_t smem = (size_t)warps * NS * kStage * sizeof(uint4);
   static_assert(NS * kStage * sizeof(uint4) >= 2 * R * (D + 2) * sizeof(float), "the ring holds the warps' results and the CTA's");
   auto kern = k_xattn_few<D, R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the most a block takes: 16 warps
+  const cudaError_t e = allow_smem<k_xattn_few<D, R>>((size_t)16 * NS * kStage * sizeof(uint4));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(grid);

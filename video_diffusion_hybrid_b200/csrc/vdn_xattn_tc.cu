@@ -598,7 +598,7 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   }
   x.status = a.status;
   const size_t smem = 1024 + (size_t)2 * BM * D * 2 + (size_t)(KST + VST) * BN * D * 2 + 40 * 8 + 16;
-  cudaError_t e = cudaFuncSetAttribute(k_xattn_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem<k_xattn_tc<D>>(smem);
   if (e != cudaSuccess) return e;
   k_xattn_tc<D><<<grid, kThr, smem, s>>>(x, mq, mk, mv);
   if ((e = cudaGetLastError()) != cudaSuccess || !c.parts) return e;
