@@ -20,9 +20,10 @@
 // The order on the tensor pipe is set so that it runs while the softmax warps
 // work.  dq: the scores are two tiles ahead (two S buffers); after dS(j) the
 // pipe has dP(j+1), dQ(j) and S(j+2), while the warps form P(j+1), which needs
-// no dP.  dkv: TMEM is full (S, dP, dV, dK), P goes over S and dS over dP:
-// after P(j) the pipe has dV(j) and S(j+1), after dS(j) it has dK(j) and
-// dP(j+1), which run under the exponentials of P(j+1).
+// no dP.  dkv: at d = 128 TMEM is full (S, dP, dV, dK), P goes over S and dS
+// over dP: after P(j) the pipe has dV(j) and S(j+1), after dS(j) it has dK(j)
+// and dP(j+1), which run under the exponentials of P(j+1).  At d = 64 there is
+// room for two score tiles, and the scores are two query tiles ahead.
 //
 // Roles (640 threads): warp 0 TMA producer, warp 1 TMEM allocator and MMA
 // issuer, warp 2 the rows' statistics, warps 4..19 softmax: four warps for each
@@ -513,10 +514,15 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
                const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   constexpr int NB = D / 64, QST = kQst, OST = kOst;
   constexpr uint32_t TILE = BR * D * 2;
-  constexpr uint32_t COL_S = 0, COL_P = 128, COL_V = 256, COL_K = 384;
+  constexpr bool TWO = D == 64;  // two S buffers, at 0 and 128
+  constexpr uint32_t COL_S = 0, COL_P = TWO ? 256 : 128, COL_V = COL_P + 128, COL_K = COL_V + D;
   enum { B_KFULL = 0, B_KEMPTY, B_VFULL, B_VEMPTY, B_QFULL, B_QEMPTY = B_QFULL + QST, B_OFULL = B_QEMPTY + QST,
-         B_OEMPTY = B_OFULL + OST, B_STFULL = B_OEMPTY + OST, B_STEMPTY = B_STFULL + 2, B_SFULL = B_STEMPTY + 2, B_P, B_PFULL, B_DS,
-         B_ACC, B_DRAIN, NBARS };
+         B_OEMPTY = B_OFULL + OST, B_STFULL = B_OEMPTY + OST, B_STEMPTY = B_STFULL + 2, B_SFULL = B_STEMPTY + 2, B_P = B_SFULL + 2,
+         B_PFULL = B_P + 2, B_DS, B_ACC, B_DRAIN, NBARS };
+  // The barriers of S and P go by buffer: with two, a softmax warp may be a query tile ahead of another at P (it is
+  // held there by dP, which waits for every warp's dS).
+  auto sbuf = [](int n) { return TWO ? n & 1 : 0; };
+  auto phase = [](int n) { return (uint32_t)(TWO ? n >> 1 : n) & 1u; };
   // the ring leaves no room for a manual alignment: the swizzled tiles need a base on 1024 bytes, which the check below asserts
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char* sK = sm;
@@ -540,7 +546,7 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
   auto bar = [&](int i) { return smem_u32(bars + i); };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBARS; ++i)
-      mbar_init(bar(i), i == B_P || i == B_DS || i == B_STEMPTY || i == B_STEMPTY + 1 ? kSoftWarps : 1);
+      mbar_init(bar(i), i == B_P || i == B_P + 1 || i == B_DS || i == B_STEMPTY || i == B_STEMPTY + 1 ? kSoftWarps : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -608,8 +614,8 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
       if (ws.j == 0 && !mbar_wait_warp(bar(B_KFULL), ws.i & 1, ctl)) return false;
       if (!mbar_wait_warp(bar(B_QFULL + sq), (ws.n / QST) & 1, ctl)) return false;
       tc_fence_after();
-      gemm_t<D>(tmem + COL_S, kd, dadd(qd, sq * TILE), el);
-      mma_commit_w(bar(B_SFULL), el);
+      gemm_t<D>(tmem + COL_S + 128 * sbuf(ws.n), kd, dadd(qd, sq * TILE), el);
+      mma_commit_w(bar(B_SFULL + sbuf(ws.n)), el);
       if (ws.last()) mma_commit_w(bar(B_KEMPTY), el);
       ws.next(x);
       return true;
@@ -625,12 +631,12 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
       wp.next(x);
       return true;
     };
-    bool ok = !ws.on || (scores() && dprod());
+    bool ok = !ws.on || (scores() && dprod() && (!TWO || !ws.on || scores()));
     for (; ok && w.on; w.next(x)) {
-      ok = mbar_wait_warp(bar(B_P), w.n & 1, ctl);
+      ok = mbar_wait_warp(bar(B_P + sbuf(w.n)), phase(w.n), ctl);
       if (!ok) break;
       tc_fence_after();
-      gemm_ts<D>(tmem + COL_V, tmem + COL_S, dadd(omn, (w.n % OST) * TILE), w.j == 0, el);  // dV += P^T dO
+      gemm_ts<D>(tmem + COL_V, tmem + COL_S + 128 * sbuf(w.n), dadd(omn, (w.n % OST) * TILE), w.j == 0, el);  // dV += P^T dO
       mma_commit_w(bar(B_OEMPTY + w.n % OST), el);
       if (ws.on && !(ok = scores())) break;  // over P^T, which the product above reads first
       ok = mbar_wait_warp(bar(B_DS), w.n & 1, ctl);
@@ -715,14 +721,16 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
       for (int j = 0; j < it.nt; ++j, ++n) {
         const float4* nl = reinterpret_cast<const float4*>(stat + 2 * (n & 1) * BR + 32 * part);
         const float4* nd = nl + BR / 4;
-        if (!mbar_wait_warp(bar(B_STFULL + (n & 1)), (n >> 1) & 1, ctl) || !mbar_wait_warp(bar(B_SFULL), n & 1, ctl)) {
+        const uint32_t sb = la + COL_S + 128 * sbuf(n) + 32 * part;
+        if (!mbar_wait_warp(bar(B_STFULL + (n & 1)), (n >> 1) & 1, ctl) ||
+            !mbar_wait_warp(bar(B_SFULL + sbuf(n)), phase(n), ctl)) {
           ok = false;
           break;
         }
         tc_fence_after();
         float p[32];
         uint32_t pk[16];
-        tmem_ld32(la + COL_S + 32 * part, p);
+        tmem_ld32(sb, p);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
@@ -740,10 +748,10 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
           if (!emit()) { ok = false; break; }
           pend = false;
         }
-        tmem_st16(la + COL_S + 32 * part, pk);
+        tmem_st16(sb, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive_warp(bar(B_P));
+        mbar_arrive_warp(bar(B_P + sbuf(n)));
         if (!mbar_wait_warp(bar(B_PFULL), n & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         float v[32];
