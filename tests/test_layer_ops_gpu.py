@@ -517,6 +517,46 @@ def test_linear_int8_refusals(cuda_ok):
         quantize_int8(x.half())
 
 
+# ---------------------------------------------------------- 16-byte alignment
+def shifted(t):
+    """A copy of t that starts 16 bytes behind a 256-byte boundary."""
+    off = 16 // t.element_size()
+    room = torch.zeros(t.numel() + off, device="cuda", dtype=t.dtype)
+    out = room[off:].view(t.shape)
+    assert out.data_ptr() % 32 == 16
+    return out.copy_(t)
+
+
+@pytest.mark.parametrize("case", [X[1], X[3], X[9], X[-3], X[10]], ids=str)
+def test_cross_attn_sixteen_byte_alignment(cuda_ok, case):
+    """Every tensor at an address of 16 mod 32: the same bits as aligned ones, forward and backward."""
+    op, q, k, v, n, _, dt = x_case(case, 60)
+    k, v, dy = k.contiguous(), v.contiguous(), rnd(gen(61), *q.shape, dtype=dt)
+    y = op(q, k, v, n).clone()
+    lse = op.lse.clone()
+    y2 = op(shifted(q), shifted(k), shifted(v), n, out=shifted(y))
+    assert torch.equal(y, y2) and torch.equal(lse, op.lse)
+    g = op.backward(q, k, v, y, lse, dy, n)
+    h = op.backward(shifted(q), shifted(k), shifted(v), shifted(y), lse, shifted(dy), n)
+    assert all(torch.equal(g[key], h[key]) for key in g)
+
+
+def test_others_sixteen_byte_alignment(cuda_ok):
+    op, a, _, _ = qk_case(QK[5], 62, skip=False)
+    q, k = a["q"].contiguous(), a["k"].contiguous()
+    rest = (a["wq"], a["wk"], a["table"], a["pos"])
+    want = op(q, k, *rest)
+    got = op(shifted(q), shifted(k), a["wq"], a["wk"], shifted(a["table"]), a["pos"], out=(shifted(q), shifted(k)))
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    g = gen(63)
+    w, ws = quantize_int8(rnd(g, 272, 1040))
+    b = rnd(g, 272)
+    for M in (1, 5, 200):
+        x = rnd(g, M, 1040, dtype=torch.bfloat16)
+        y = Int8Linear(w, ws, b)(x)
+        assert torch.equal(y, Int8Linear(shifted(w), shifted(ws), shifted(b))(shifted(x), out=shifted(y)))
+
+
 # ------------------------------------------------- together, streams, graphs
 class Layer:
     """Projection -> norm and rotation -> cross-attention -> 8-bit output layer."""
