@@ -191,3 +191,28 @@ def test_null_structs():
     for fn in ("vdn_qk_norm_rope_bwd_workspace_size", "vdn_cross_attn_workspace_size", "vdn_cross_attn_bwd_workspace_size",
                "vdn_linear_int8_workspace_size"):
         assert getattr(lib, fn)(None) == 0
+
+
+@pytest.mark.parametrize("kw,fwd,bwd", [
+    (dict(), 1, 1), (dict(Tq=4), 2, 1), (dict(Tq=5), 1, 1), (dict(Tq=1, H=8, Hkv=1), 2, 1), (dict(Tq=1, H=9, Hkv=1), 1, 1),
+    (dict(d=32), 0, 0), (dict(dtype=L.VDN_F32), 0, 0), (dict(Tq=1, d=32), 0, 0), (dict(Tq=1, dtype=L.VDN_F32), 0, 0),
+], ids=str)
+def test_xattn_implementation(kw, fwd, bwd):
+    """bf16 of d = 64 or 128: up to 8 query rows a key head take the kernel for few rows, more the tensor cores."""
+    cfg = x_cfg(**kw)
+    assert (L.vdn_cross_attn_impl(cfg), L.vdn_cross_attn_impl(cfg, True)) == (fwd, bwd)
+
+
+def test_xattn_workspace_sizes():
+    """Status words alone where nothing is split; few rows need no more however long the states are."""
+    assert L.vdn_cross_attn_workspace_size(x_cfg(Tq=1, L=1 << 20)) == 256
+    assert L.vdn_cross_attn_workspace_size(x_cfg(B=40, Tq=4000)) == 256
+    assert L.vdn_cross_attn_workspace_size(x_cfg(B=1, Tq=64, L=8192)) > 256
+    rows = 2 * 100 * 8
+    assert L.vdn_cross_attn_bwd_workspace_size(x_cfg()) >= 256 + 4 * rows
+
+
+def test_int8_workspace_is_for_codes_and_scales():
+    assert L.vdn_linear_int8_workspace_size(i8_cfg(M=8)) == 0
+    assert L.vdn_linear_int8_workspace_size(i8_cfg(M=9)) >= 9 * 64 + 9 * 4
+    assert L.vdn_linear_int8_workspace_size(i8_cfg(M=1 << 20, K=131056)) >= (1 << 20) * (131056 + 4)

@@ -479,15 +479,8 @@ vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const floa
 }
 
 uint32_t* status_of_proj() {
-  // the symbol's address on each device, looked up once
-  static std::atomic<void*> at[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-  void* p = dev < 64 ? at[dev].load(std::memory_order_relaxed) : nullptr;
-  if (p == nullptr) {
-    if (cudaGetSymbolAddress(&p, g_proj_status) != cudaSuccess) return nullptr;
-    if (dev < 64) at[dev].store(p, std::memory_order_relaxed);
-  }
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_proj_status) != cudaSuccess) return nullptr;
   return static_cast<uint32_t*>(p);
 }
 

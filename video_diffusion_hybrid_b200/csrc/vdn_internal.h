@@ -1,7 +1,6 @@
 // Internal declarations shared by the library's translation units.
 #pragma once
 
-#include <atomic>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -105,18 +104,10 @@ cudaError_t launch_scan256_tc(const Dims& d, const Inputs& in, const Work& w, cu
 // scales != nullptr: e4m3 y [M, K] and w [N, K], dequantisation scales {s_y, s_w} in device memory
 vdn_status out_proj(int M, int K, int N, int out_dtype, const void* y, const void* w, void* out, cudaStream_t s,
                     const float* scales = nullptr);
-// A kernel's limit of dynamic shared memory raised to `bytes`, once for each device (0.5 us a call saved).
+// A kernel's limit of dynamic shared memory, on the current device (every call: a device reset drops it).
 template <auto Kernel>
 cudaError_t allow_smem(size_t bytes) {
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ULL << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
+  return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 // device address of the projection's status words (library-owned), or null
 uint32_t* status_of_proj();
