@@ -165,6 +165,13 @@ def test_qk_refusals(cuda_ok):
                 dict(pos=a["pos"][:-1]), dict(q=a["q"].cpu())):
         with pytest.raises((ValueError, TypeError)):
             call(**bad)
+    for missing in ("q", "k", "table"):
+        with pytest.raises((ValueError, TypeError)):
+            call(**{missing: None})
+    up = [torch.zeros_like(a[key]) for key in "qk"]
+    for bad in ((None, up[1]), (up[0], None), (up[0].double(), up[1]), (up[0][:-1], up[1]), (up[0], up[1].bfloat16())):
+        with pytest.raises((ValueError, TypeError)):
+            op.backward(a["q"], a["k"], a["wq"], a["wk"], a["table"], *bad, a["pos"])
     with pytest.raises(L.VdnError):
         QKNormRope(8, 2, 64, pairing="other")
     with pytest.raises(L.VdnError):
@@ -271,6 +278,13 @@ def test_cross_attn_backward(cuda_ok, case):
         m = max(m, 0)
         assert bool((got["dk"][b, m:] == 0).all()) and bool((got["dv"][b, m:] == 0).all())
         assert m > 0 or bool((got["dq"][b] == 0).all())
+
+
+@pytest.mark.parametrize("case", [X[1], X[9], X[-3]], ids=str)
+def test_cross_attn_tiny_scale(cuda_ok, case):
+    """Scores of zero in effect: every weight alike, the log-sum-exp that of the number of states."""
+    op, q, k, v, n, clean, dt = x_case(case, 70, scale=1e-38)
+    x_forward_check(op, q, *clean, n, dt, op(q, k, v, n), 1e-38)
 
 
 @pytest.mark.parametrize("case", [X[2], X[9], X[-3]], ids=str)
@@ -403,9 +417,12 @@ def test_cross_attn_refusals(cuda_ok):
             op.backward(bad[0], bad[1], bad[2], q, lse, dy, bad[3])
     with pytest.raises(ValueError):
         op(q, k, v, n, out=torch.empty_like(q).float())
-    for kw in (dict(y=q.float()), dict(lse=lse.double()), dict(dy=dy[:1])):
+    for bad in ((None, k, v), (q, None, v), (q, k, None)):
+        with pytest.raises(TypeError):
+            op(*bad)
+    for kw in (dict(y=q.float()), dict(lse=lse.double()), dict(dy=dy[:1]), dict(y=None), dict(lse=None), dict(dy=None)):
         a = {**dict(y=q, lse=lse, dy=dy), **kw}
-        with pytest.raises(ValueError):
+        with pytest.raises((ValueError, TypeError)):
             op.backward(q, k, v, a["y"], a["lse"], a["dy"], n)
     for shape in ((0, 1, 1, 1, 1, 64), (1, 1, 1, 3, 2, 64), (1, 1, 1, 1, 1, 48)):
         with pytest.raises(L.VdnError):

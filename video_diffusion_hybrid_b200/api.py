@@ -215,6 +215,11 @@ def _dtype_of(t: torch.Tensor) -> int:
     raise TypeError(f"bfloat16 or float32 expected, got {t.dtype}")
 
 
+def _given(t, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor is needed, got {type(t).__name__}")
+
+
 def _need(t, name: str, shape, dtype, device) -> None:
     """A dense tensor of this shape, type and device (None passes)."""
     if t is None:
@@ -228,6 +233,7 @@ def _head_rows(t: torch.Tensor, name: str, lead: tuple, H: int, d: int, dtype, d
     """Checks a [*lead, H, d] tensor whose head rows are dense and whose tokens
     lie one stride apart (a slice of a packed projection); returns that stride
     in elements."""
+    _given(t, name)
     shape, strides = t.shape, t.stride()
     if shape != (*lead, H, d) or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {(*lead, H, d)} on {device}, got {t.dtype} {tuple(shape)} on {t.device}")
@@ -302,6 +308,7 @@ class QKNormRope(_Streamed):
         self.wq_shape, self.wk_shape = ((Hq, d), (Hk, d)) if per_head else ((d,), (d,))
 
     def _cfg_args(self, q, k, wq, wk, table, pos, grad=0):
+        _given(q, "q")
         lead, dt, dev = q.shape[:-2], q.dtype, self.device
         qs = _head_rows(q, "q", lead, self.Hq, self.d, dt, dev)
         ks = _head_rows(k, "k", lead, self.Hk, self.d, dt, dev) if self.Hk else 0
@@ -339,9 +346,11 @@ class QKNormRope(_Streamed):
     def backward(self, q, k, wq, wk, table, dq_out, dk_out, pos=None, stream=None) -> dict:
         """dq, dk (q's type) and dwq, dwk (float32) from the gradients of the
         outputs (float32, or q's type)."""
+        _given(dq_out, "dq_out")
         cfg, args = self._cfg_args(q, k, wq, wk, table, pos, _dtype_of(dq_out))
         _need(dq_out, "dq_out", q.shape, dq_out.dtype, self.device)
         if self.Hk:
+            _given(dk_out, "dk_out")
             _need(dk_out, "dk_out", k.shape, dq_out.dtype, self.device)
         ws = self._new(L.vdn_qk_norm_rope_bwd_workspace_size(cfg), torch.uint8, stream)
         new = lambda shape, dt: self._new(shape, dt, stream)  # noqa: E731
@@ -387,6 +396,7 @@ class CrossAttention(_Streamed):
 
     def _inputs(self, q, k, v, kv_len):
         B, _, Hkv, d = self.kv_shape
+        _given(q, "q")
         _need(q, "q", self.shape, self.torch_dtype, self.device)
         _need(kv_len, "kv_len", (B,), torch.int32, self.device)
         key = (_head_rows(k, "k", self.kv_shape[:2], Hkv, d, self.torch_dtype, self.device),
@@ -410,6 +420,8 @@ class CrossAttention(_Streamed):
     def backward(self, q, k, v, y, lse, dy, kv_len=None, stream=None) -> dict:
         """dq, dk, dv from the forward's output y and log-sum-exp."""
         cfg, a = self._inputs(q, k, v, kv_len)
+        for t, name in ((y, "y"), (lse, "lse"), (dy, "dy")):
+            _given(t, name)
         _need(y, "y", self.shape, self.torch_dtype, self.device)
         _need(dy, "dy", self.shape, self.torch_dtype, self.device)
         _need(lse, "lse", self.shape[:3], torch.float32, self.device)
@@ -458,6 +470,7 @@ class Int8Linear(_Streamed):
         self.out_dtype = L.VDN_BF16 if out_dtype == "bf16" else L.VDN_F32
 
     def __call__(self, x: torch.Tensor, x_scale=None, out=None, stream=None) -> torch.Tensor:
+        _given(x, "x")
         codes = x.dtype == torch.int8
         if x.shape[-1] != self.K or not x.is_contiguous() or x.device != self.device:
             raise ValueError(f"Int8Linear: expected a contiguous [..., {self.K}] tensor on {self.device}")

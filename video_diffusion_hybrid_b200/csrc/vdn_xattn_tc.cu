@@ -325,7 +325,7 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t scol = lane_addr + col_s(t), ocol = lane_addr + col_o(t);
     const float c = x.scale * kLog2e;       // log2 units
-    const float thresh = kRescaleLog2 / c;  // raw scores
+    const float thresh = fminf(kRescaleLog2 / c, 1e30f);  // raw scores; finite, so that a first maximum is always taken
     const int rtok = row / x.P, rhead = row % x.P;
     const bool whole = (reinterpret_cast<uintptr_t>(x.y) & 31) == 0;
     int n = 0;  // key tiles of this tile so far
