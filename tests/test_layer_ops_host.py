@@ -194,11 +194,11 @@ def test_null_structs():
 
 
 @pytest.mark.parametrize("kw,fwd,bwd", [
-    (dict(), 1, 1), (dict(Tq=4), 2, 1), (dict(Tq=5), 1, 1), (dict(Tq=1, H=8, Hkv=1), 2, 1), (dict(Tq=1, H=9, Hkv=1), 1, 1),
+    (dict(), 1, 1), (dict(Tq=8), 2, 1), (dict(Tq=9), 1, 1), (dict(Tq=1, H=16, Hkv=1), 2, 1), (dict(Tq=1, H=17, Hkv=1), 1, 1),
     (dict(d=32), 0, 0), (dict(dtype=L.VDN_F32), 0, 0), (dict(Tq=1, d=32), 0, 0), (dict(Tq=1, dtype=L.VDN_F32), 0, 0),
 ], ids=str)
 def test_xattn_implementation(kw, fwd, bwd):
-    """bf16 of d = 64 or 128: up to 8 query rows a key head take the kernel for few rows, more the tensor cores."""
+    """bf16 of d = 64 or 128: up to 16 query rows a key head take the kernel for few rows, more the tensor cores."""
     cfg = x_cfg(**kw)
     assert (L.vdn_cross_attn_impl(cfg), L.vdn_cross_attn_impl(cfg, True)) == (fwd, bwd)
 

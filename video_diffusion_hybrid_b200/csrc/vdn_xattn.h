@@ -71,7 +71,7 @@ cudaError_t launch_xattn_simt(const XDims& d, const XArgs& a, bool bf16, cudaStr
 size_t xattn_simt_bwd_scratch(const XDims& d);
 cudaError_t launch_xattn_simt_bwd(const XDims& d, const XArgs& a, bool bf16, cudaStream_t s);
 
-// bf16, d = 64 or 128, up to 8 query rows for a key head (vdn_xattn_few.cu); no scratch
+// bf16, d = 64 or 128, up to 16 query rows for a key head (vdn_xattn_few.cu); no scratch
 bool xattn_few_supported(const XDims& d);
 cudaError_t launch_xattn_few(const XDims& d, const XArgs& a, cudaStream_t s);
 

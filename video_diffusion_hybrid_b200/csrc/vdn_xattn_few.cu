@@ -1,28 +1,31 @@
 // Cross-attention for few query rows (a token of a stream, a short draft): all
-// rows that share a key head, up to 8, against its states.  bf16 in and out,
-// fp32 arithmetic.
+// rows that share a key head, up to 16, against its states.  bf16 in and out,
+// fp32 scores, softmax and accumulation.
 //
 // Bound by the read of k and v, once.  The states of a key head are split over
-// a cluster of up to 8 CTAs, over their warps, and over the D / 8 lanes that
-// hold a state's row with 8 columns each; every group of lanes keeps a running
-// maximum, sum and output of its own (no exchange inside the loop but the sums
-// of a score), with the next states' k and v on their way into shared memory
-// (cp.async; a lane copies what it reads itself, so there are no barriers).
+// a cluster of up to 8 CTAs and over their warps.  A warp takes 16 states at a
+// time from a ring of its own in shared memory (cp.async, so that the next
+// ones are on their way; no block barrier), forms the 16 x 16 scores and adds
+// P V with warp-level matrix products (16 rows are the smallest tile those
+// have, and all that there are; with the 128 rows of a tcgen05 tile this took
+// 39 us where it takes @@ now), and keeps a running maximum, sum and output.
 // At the end the warps' results are joined across the cluster through
 // distributed shared memory: one launch, no scratch.
-// A row of a tensor-core tile would be one of 128: the tile kernel took 39 us
-// where this one takes 20 (8 requests of 1,408 to 4,096 states, 8 key heads of
-// 3 queries, d = 128, nothing in L2), most of it the fetch of its longer code.
+// (Dot products on the FMA pipe, a row of k in 16 lanes, took 31 us: the sums
+// over lanes alone are 48 shuffles for 8 states and 3 rows.)
 #include <cuda_bf16.h>
 
+#include "tc_common.cuh"
 #include "vdn_xattn.h"
 
 namespace vdn {
 namespace {
+using tc::ex2;
+using tc::pack_bf16;
 
-constexpr int NS = 3;             // stages of a warp's ring
-constexpr int U = 4;              // states of a group of lanes in a stage
-constexpr int kStage = 2 * U * 32;  // uint4 of a warp's stage: k and v
+constexpr int NS = 3;      // stages of a warp's ring
+constexpr int KT = 16;     // states of a stage
+constexpr int ROWS = 16;   // query rows of a key head
 constexpr int kMaxCluster = 8;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
@@ -42,23 +45,20 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)
 __device__ __forceinline__ void copy16(uint4* dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
+// four 8 x 8 blocks of 16-bit values, lane l giving the address of row l % 8 of block l / 8
+__device__ __forceinline__ void blocks4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+__device__ __forceinline__ void blocks4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void expand(const uint4& u, float2 (&x)[4]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+// c (16 x 8) += a (16 x 16) b (16 x 8), bf16 with fp32 sums
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // the float at this shared address in CTA `rank` of the cluster
 __device__ __forceinline__ float remote(const float* p, int rank) {
@@ -72,164 +72,160 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int D, int R>
-__global__ void __launch_bounds__(R > 4 ? 256 : 512) k_xattn_few(const XfDev x) {
-  constexpr int LPK = D / 8, KPW = 32 / LPK, STEP = U * KPW;  // lanes a state, states a warp has at once, and in a stage
+template <int D> constexpr int stage_chunks() { return 2 * KT * D / 8; }  // 16-byte chunks: k, then v
+template <int D> constexpr int most_warps() { return D == 128 ? 8 : 16; }
+template <int D> constexpr size_t warp_smem() { return (size_t)NS * stage_chunks<D>() * 16; }
+
+template <int D>
+__global__ void __launch_bounds__(32 * most_warps<D>()) k_xattn_few(const XfDev x) {
+  constexpr int CPR = D / 8, KPI = 32 / CPR;  // chunks of a row, rows a warp copies at once
   extern __shared__ uint4 ring[];
   clear_status(x.status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  const int li = lane % LPK, grp = lane / LPK;
+  const int g = lane >> 2, t2 = 2 * (lane & 3);  // of a 16 x 8 result: rows g and g + 8, columns t2 and t2 + 1
   const int rank = blockIdx.x % x.ns, bh = blockIdx.x / x.ns, Hkv = x.H / x.G, b = bh / Hkv, hk = bh % Hkv;
   int n = x.L;
   if (x.kv_len != nullptr) n = max(0, min(__ldg(x.kv_len + b), x.L));
   // this CTA's states, in whole stages
-  const int all = (n + STEP - 1) / STEP, per = (all + x.ns - 1) / x.ns, lo = min(rank * per, all), hi = min(lo + per, all);
-  const __nv_bfloat16* kp = x.k + (long long)b * x.L * x.ks + hk * D + 8 * li;
-  const __nv_bfloat16* vp = x.v + (long long)b * x.L * x.vs + hk * D + 8 * li;
-  uint4* mine = ring + warp * NS * kStage + lane;
+  const int all = (n + KT - 1) / KT, per = (all + x.ns - 1) / x.ns, lo = min(rank * per, all), hi = min(lo + per, all);
+  uint4* mine = ring + warp * NS * stage_chunks<D>();
+  const int ck = lane % CPR, rk = lane / CPR;  // the chunk and the first row that this lane copies
+  const __nv_bfloat16* kp = x.k + ((long long)b * x.L + rk) * x.ks + hk * D + 8 * ck;
+  const __nv_bfloat16* vp = x.v + ((long long)b * x.L + rk) * x.vs + hk * D + 8 * ck;
+  // chunk c of row r lies at c ^ (r % 8): the eight rows of a block in eight different groups of banks
   auto fetch = [&](int stage, int it) {
+    uint4* sk = mine + stage * stage_chunks<D>();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long key = (long long)it * STEP + u * KPW + grp;
-      const bool on = it < hi && key < n;
-      copy16(mine + stage * kStage + u * 32, on ? kp + key * x.ks : kp, on);
-      copy16(mine + stage * kStage + (U + u) * 32, on ? vp + key * x.vs : vp, on);
+    for (int i = 0; i < KT / KPI; ++i) {
+      const int r = rk + i * KPI;
+      const long long key = (long long)it * KT + i * KPI;
+      const bool on = it < hi && it * KT + r < n;
+      uint4* dst = sk + r * CPR + (ck ^ (r & 7));
+      copy16(dst, on ? kp + key * x.ks : x.k, on);
+      copy16(dst + KT * CPR, on ? vp + key * x.vs : x.v, on);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int it = lo + warp;
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) fetch(s, it + s * nw);
-  // the rows, times scale and log2 e
-  float2 q[R][4], o[R][4];
-  float m[R], l[R];
-  const float c = x.scale * kLog2e;
+  // the query rows as left operands: rows g and g + 8, columns t2 and t2 + 8 of every 16
+  uint32_t qa[D / 16][4];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (r < x.rows)
-      raw = __ldg(reinterpret_cast<const uint4*>(x.q + (((long long)b * x.Tq + r / x.G) * x.H + hk * x.G + r % x.G) * D + 8 * li));
-    expand(raw, q[r]);
+  for (int h = 0; h < 2; ++h) {
+    const int r = g + 8 * h;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(x.q + (((long long)b * x.Tq + r / x.G) * x.H + hk * x.G + r % x.G) * D + t2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[r][i].x *= c;
-      q[r][i].y *= c;
-      o[r][i] = make_float2(0.f, 0.f);
+    for (int i = 0; i < D / 16; ++i) {
+      qa[i][h] = r < x.rows ? __ldg(p + 8 * i) : 0u;
+      qa[i][h + 2] = r < x.rows ? __ldg(p + 8 * i + 4) : 0u;
     }
   }
+  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  const float c = x.scale * kLog2e;
   int st = 0;
 #pragma unroll 1
   for (; it < hi; it += nw) {
+    __syncwarp();  // the stage filled next was read by every lane
     fetch(st == 0 ? NS - 1 : st - 1, it + (NS - 1) * nw);
     asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
-    const uint4* at = mine + st * kStage;
+    __syncwarp();
+    const uint4* sk = mine + st * stage_chunks<D>();
+    const uint4* sv = sk + KT * CPR;
     st = st + 1 == NS ? 0 : st + 1;
-    float s[U][R];
+    // scores of states 0..7 and 8..15, two chains each
+    float s[2][2][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float2 k[4];
-      expand(at[u * 32], k);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float2 a = make_float2(0.f, 0.f);
+      for (int e = 0; e < 4; ++e) s[j][0][e] = s[j][1][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a = fma2(k[i], q[r][i], a);
-        s[u][r] = a.x + a.y;
+    for (int j = 0; j < 2; ++j) {
+      const int r = 8 * j + (lane & 7);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t kb[4];
+        blocks4(kb, smem_addr(sk + r * CPR + ((4 * i + (lane >> 3)) ^ (r & 7))));
+        mma16(s[j][0], qa[2 * i], kb[0], kb[1]);
+        mma16(s[j][1], qa[2 * i + 1], kb[2], kb[3]);
       }
     }
+    uint32_t pa[4];
+    float f[2];
 #pragma unroll
-    for (int w = LPK / 2; w > 0; w >>= 1)
+    for (int h = 0; h < 2; ++h) {
+      float z[4], mx = m[h];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int r = 0; r < R; ++r) s[u][r] += __shfl_xor_sync(0xffffffffu, s[u][r], w);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if ((long long)it * STEP + u * KPW + grp >= n) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) s[u][r] = -INFINITY;
+      for (int e = 0; e < 4; ++e) {
+        const int key = it * KT + 8 * (e >> 1) + t2 + (e & 1);
+        z[e] = (s[e >> 1][0][2 * h + (e & 1)] + s[e >> 1][1][2 * h + (e & 1)]) * c;
+        if (key >= n) z[e] = -INFINITY;
+        mx = fmaxf(mx, z[e]);
       }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float mx = m[r];
-#pragma unroll
-      for (int u = 0; u < U; ++u) mx = fmaxf(mx, s[u][r]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       // no score above -inf so far: the reference stays at zero, weights of 0 and not of inf - inf
-      const float ref = mx == -INFINITY ? 0.f : mx, f = ex2(m[r] - ref);
-      m[r] = mx;
-      l[r] *= f;
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      f[h] = ex2(m[h] - ref);
+      m[h] = mx;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[r][i].x *= f;
-        o[r][i].y *= f;
-      }
+      for (int e = 0; e < 4; ++e) z[e] = ex2(z[e] - ref);
+      l[h] = fmaf(l[h], f[h], (z[0] + z[1]) + (z[2] + z[3]));
+      pa[h] = pack_bf16(z[0], z[1]);      // the product's operand type; l adds the unrounded weights
+      pa[h + 2] = pack_bf16(z[2], z[3]);
+    }
+    if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        s[u][r] = ex2(s[u][r] - ref);
-        l[r] += s[u][r];
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= f[0];
+        o[i][1] *= f[0];
+        o[i][2] *= f[1];
+        o[i][3] *= f[1];
       }
     }
+    const int r = lane & 15;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float2 v[4];
-      expand(at[(U + u) * 32], v);
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[r][i] = fma2(make_float2(s[u][r], s[u][r]), v[i], o[r][i]);
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t vb[4];
+      blocks4_t(vb, smem_addr(sv + r * CPR + ((2 * i + (lane >> 4)) ^ (r & 7))));
+      mma16(o[2 * i], pa, vb[0], vb[1]);
+      mma16(o[2 * i + 1], pa, vb[2], vb[3]);
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  // the groups of a warp
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int w = LPK; w < 32; w <<= 1) {
-      const float mo = __shfl_xor_sync(0xffffffffu, m[r], w), mx = fmaxf(m[r], mo), ref = mx == -INFINITY ? 0.f : mx;
-      const float f = ex2(m[r] - ref);
-      m[r] = mx;
-      l[r] *= f;
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[r][i].x *= f;
-        o[r][i].y *= f;
-        o[r][i].x += __shfl_xor_sync(0xffffffffu, o[r][i].x, w);
-        o[r][i].y += __shfl_xor_sync(0xffffffffu, o[r][i].y, w);
-      }
-    }
-  }
-  // the warps' results in shared memory: [warp][R][D + 2] = o, m, l; then the CTA's, [R][D + 2] behind them
+  // the warps' results in shared memory: [warp][rows][D + 2] = o, m, l; then the CTA's, [rows][D + 2] behind them
   __syncthreads();
   constexpr int RW = D + 2;
   float* res = reinterpret_cast<float*>(ring);
-  float* cta = res + nw * R * RW;
+  float* cta = res + nw * x.rows * RW;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float* p = res + (warp * R + r) * RW;
-    if (grp == 0) {
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    if (g + 8 * h < x.rows) {
+      float* p = res + (warp * x.rows + g + 8 * h) * RW;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(p + 8 * li + 2 * i) = o[r][i];
-      if (li == 0) {
-        p[D] = m[r];
-        p[D + 1] = l[r];
+      for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(p + 8 * i + t2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+      if (t2 == 0) {
+        p[D] = m[h];
+        p[D + 1] = l[h];
       }
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < R * D; i += blockDim.x) {
+  for (int i = threadIdx.x; i < x.rows * D; i += blockDim.x) {
     const int r = i / D, col = i % D;
     float mx = -INFINITY;
-    for (int w = 0; w < nw; ++w) mx = fmaxf(mx, res[(w * R + r) * RW + D]);
+    for (int w = 0; w < nw; ++w) mx = fmaxf(mx, res[(w * x.rows + r) * RW + D]);
     const float ref = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f, out = 0.f;
     for (int w = 0; w < nw; ++w) {
-      const float* p = res + (w * R + r) * RW;
-      const float f = ex2(p[D] - ref);
-      sum = fmaf(f, p[D + 1], sum);
-      out = fmaf(f, p[col], out);
+      const float* p = res + (w * x.rows + r) * RW;
+      const float e = ex2(p[D] - ref);
+      sum = fmaf(e, p[D + 1], sum);
+      out = fmaf(e, p[col], out);
     }
     cta[r * RW + col] = out;
     if (col == 0) {
@@ -257,9 +253,9 @@ __global__ void __launch_bounds__(R > 4 ? 256 : 512) k_xattn_few(const XfDev x) 
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k)
       if (k < x.ns) {
-        const float f = ex2(pm[k] - ref);
-        sum = fmaf(f, pl[k], sum);
-        out = fmaf(f, po[k], out);
+        const float e = ex2(pm[k] - ref);
+        sum = fmaf(e, pl[k], sum);
+        out = fmaf(e, po[k], out);
       }
     const long long row = ((long long)b * x.Tq + r / x.G) * x.H + hk * x.G + r % x.G;
     x.y[row * D + col] = __float2bfloat16_rn(n > 0 ? out / sum : 0.f);
@@ -268,40 +264,36 @@ __global__ void __launch_bounds__(R > 4 ? 256 : 512) k_xattn_few(const XfDev x) 
   cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
-template <int D, int R>
-cudaError_t launch(const XfDev& x, int warps, unsigned grid, cudaStream_t s) {
-  const size_t smem = (size_t)warps * NS * kStage * sizeof(uint4);
-  static_assert(NS * kStage * sizeof(uint4) >= 2 * R * (D + 2) * sizeof(float), "the ring holds the warps' results and the CTA's");
-  auto kern = k_xattn_few<D, R>;
-  // the most a block takes: 16 warps
-  const cudaError_t e = allow_smem<k_xattn_few<D, R>>((size_t)16 * NS * kStage * sizeof(uint4));
+template <int D>
+cudaError_t launch(XfDev x, cudaStream_t s) {
+  // A ring of 24 KB (d = 128) a warp: two CTAs of 4 warps on an SM, or one of 8.  The states are split over as many CTAs
+  // as still run at once, while a warp has two stages or more.
+  constexpr int W = most_warps<D>() / 2;
+  const long long base = (long long)x.B * (x.H / x.G);
+  const int stages = (x.L + KT - 1) / KT;
+  x.ns = 1;
+  while (x.ns < kMaxCluster && base * 2 * x.ns <= 2 * 148 && stages >= 2 * x.ns * 2 * W) x.ns *= 2;
+  const int warps = base * x.ns <= 148 ? 2 * W : W;
+  static_assert(warp_smem<D>() >= 2 * ROWS * (D + 2) * sizeof(float), "the ring holds the warps' results and the CTA's");
+  const cudaError_t e = allow_smem<k_xattn_few<D>>(most_warps<D>() * warp_smem<D>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(grid);
+  lc.gridDim = dim3((unsigned)(base * x.ns));
   lc.blockDim = dim3(32 * warps);
-  lc.dynamicSmemBytes = smem;
+  lc.dynamicSmemBytes = warps * warp_smem<D>();
   lc.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim = {(unsigned)x.ns, 1, 1};
   lc.attrs = at;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, kern, x);
-}
-
-template <int D>
-cudaError_t pick(const XfDev& x, int warps, unsigned grid, cudaStream_t s) {
-  if (x.rows == 1) return launch<D, 1>(x, warps, grid, s);
-  if (x.rows == 2) return launch<D, 2>(x, warps, grid, s);
-  if (x.rows == 3) return launch<D, 3>(x, warps, grid, s);
-  if (x.rows == 4) return launch<D, 4>(x, warps, grid, s);
-  return launch<D, 8>(x, warps, grid, s);
+  return cudaLaunchKernelEx(&lc, k_xattn_few<D>, x);
 }
 
 }  // namespace
 
 bool xattn_few_supported(const XDims& d) {
-  return (d.d == 64 || d.d == 128) && (long long)d.Tq * d.G <= 8 && (long long)d.B * d.Hkv <= (1LL << 31) / kMaxCluster - 1;
+  return (d.d == 64 || d.d == 128) && (long long)d.Tq * d.G <= ROWS && (long long)d.B * d.Hkv <= (1LL << 31) / kMaxCluster - 1;
 }
 
 cudaError_t launch_xattn_few(const XDims& d, const XArgs& a, cudaStream_t s) {
@@ -316,15 +308,7 @@ cudaError_t launch_xattn_few(const XDims& d, const XArgs& a, cudaStream_t s) {
   x.y = static_cast<__nv_bfloat16*>(const_cast<void*>(a.y));
   x.lse = a.lse;
   x.status = a.status;
-  // CTAs of 4 warps while they fill the SMs (up to 4 on each); fewer key heads get more warps each.  A CTA has four
-  // stages of states a warp at least where there are several.
-  const long long base = (long long)d.B * d.Hkv;
-  const int stages = (d.L + U * 32 / (d.d / 8) - 1) / (U * 32 / (d.d / 8));
-  x.ns = 1;
-  while (x.ns < kMaxCluster && base * x.ns < 4 * 148 && stages >= 2 * x.ns * 16) x.ns *= 2;
-  const int warps = base * x.ns <= 148 && x.rows <= 4 ? 16 : base * x.ns <= 296 ? 8 : 4;
-  const unsigned grid = (unsigned)(base * x.ns);
-  return d.d == 128 ? pick<128>(x, warps, grid, s) : pick<64>(x, warps, grid, s);
+  return d.d == 128 ? launch<128>(x, s) : launch<64>(x, s);
 }
 
 }  // namespace vdn
