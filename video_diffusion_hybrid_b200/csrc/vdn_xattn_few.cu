@@ -8,7 +8,7 @@
 // ones are on their way; no block barrier), forms the 16 x 16 scores and adds
 // P V with warp-level matrix products (16 rows are the smallest tile those
 // have, and all that there are; with the 128 rows of a tcgen05 tile this took
-// 39 us where it takes @@ now), and keeps a running maximum, sum and output.
+// 39 us where this takes 28), and keeps a running maximum, sum and output.
 // At the end the warps' results are joined across the cluster through
 // distributed shared memory: one launch, no scratch.
 // (Dot products on the FMA pipe, a row of k in 16 lanes, took 31 us: the sums
