@@ -5,10 +5,13 @@
 // Bound by the read of k and v, once.  The states of a key head are split over
 // a cluster of up to 8 CTAs and over their warps.  A warp takes 16 states at a
 // time from a ring of its own in shared memory (cp.async, so that the next
-// ones are on their way; no block barrier), forms the 16 x 16 scores and adds
-// P V with warp-level matrix products (16 rows are the smallest tile those
-// have, and all that there are; with the 128 rows of a tcgen05 tile this took
-// 39 us where this takes 28), and keeps a running maximum, sum and output.
+// ones are on their way; no block barrier), forms the scores of 8 or 16 rows and
+// adds P V with warp-level matrix products, and keeps a running reference, sum
+// and output.  Both products have the states or columns as their 16 rows and
+// the query rows as their 8 columns (S^T = K q^T, O^T = V^T P^T), which is the
+// finest step in query rows there is: with the query rows as the 16 rows of
+// the result it took 28 us where this took 20.5, with the 128 rows of a tcgen05
+// tile 39.
 // At the end the warps' results are joined across the cluster through
 // distributed shared memory: one launch, no scratch.
 // (Dot products on the FMA pipe, a row of k in 16 lanes, took 31 us: the sums
@@ -27,6 +30,7 @@ constexpr int NS = 3;      // stages of a warp's ring
 constexpr int KT = 16;     // states of a stage
 constexpr int ROWS = 16;   // query rows of a key head
 constexpr int kMaxCluster = 8;
+constexpr float kSlack = 8.f;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 struct XfDev {
@@ -42,17 +46,27 @@ struct XfDev {
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void copy16(uint4* dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {  // off: 16 bytes of zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 // four 8 x 8 blocks of 16-bit values, lane l giving the address of row l % 8 of block l / 8
 __device__ __forceinline__ void blocks4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+// the same transposed, blocks 1 and 2 swapped
 __device__ __forceinline__ void blocks4_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+               : "=r"(r[0]), "=r"(r[2]), "=r"(r[1]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// the transpose of an 8 x 8 block spread over the warp as a result is
+__device__ __forceinline__ uint32_t turned(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 // c (16 x 8) += a (16 x 16) b (16 x 8), bf16 with fp32 sums
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -76,9 +90,12 @@ template <int D> constexpr int stage_chunks() { return 2 * KT * D / 8; }  // 16-
 template <int D> constexpr int most_warps() { return D == 128 ? 8 : 16; }
 template <int D> constexpr size_t warp_smem() { return (size_t)NS * stage_chunks<D>() * 16; }
 
-template <int D>
+// NB: blocks of 8 query rows
+template <int D, int NB>
 __global__ void __launch_bounds__(32 * most_warps<D>()) k_xattn_few(const XfDev x) {
   constexpr int CPR = D / 8, KPI = 32 / CPR;  // chunks of a row, rows a warp copies at once
+  constexpr int TURN = 8 / KPI;               // copies until the rows' places repeat
+  constexpr uint32_t ROW = CPR * 16, HALF = KT * ROW, STAGE = 2 * HALF;
   extern __shared__ uint4 ring[];
   clear_status(x.status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
@@ -88,111 +105,143 @@ __global__ void __launch_bounds__(32 * most_warps<D>()) k_xattn_few(const XfDev 
   if (x.kv_len != nullptr) n = max(0, min(__ldg(x.kv_len + b), x.L));
   // this CTA's states, in whole stages
   const int all = (n + KT - 1) / KT, per = (all + x.ns - 1) / x.ns, lo = min(rank * per, all), hi = min(lo + per, all);
-  uint4* mine = ring + warp * NS * stage_chunks<D>();
+  const uint32_t mine = smem_addr(ring) + warp * NS * STAGE;
   const int ck = lane % CPR, rk = lane / CPR;  // the chunk and the first row that this lane copies
-  const __nv_bfloat16* kp = x.k + ((long long)b * x.L + rk) * x.ks + hk * D + 8 * ck;
-  const __nv_bfloat16* vp = x.v + ((long long)b * x.L + rk) * x.vs + hk * D + 8 * ck;
+  int it = lo + warp, next = it;               // the stage worked on, and the one to copy
+  const long long first = (long long)b * x.L + (long long)it * KT + rk, kstep = KPI * x.ks * 2, vstep = KPI * x.vs * 2;
+  const char* kp = reinterpret_cast<const char*>(x.k + first * x.ks + hk * D + 8 * ck);
+  const char* vp = reinterpret_cast<const char*>(x.v + first * x.vs + hk * D + 8 * ck);
   // chunk c of row r lies at c ^ (r % 8): the eight rows of a block in eight different groups of banks
-  auto fetch = [&](int stage, int it) {
-    uint4* sk = mine + stage * stage_chunks<D>();
+  uint32_t to[TURN], from[4];
 #pragma unroll
-    for (int i = 0; i < KT / KPI; ++i) {
-      const int r = rk + i * KPI;
-      const long long key = (long long)it * KT + i * KPI;
-      const bool on = it < hi && it * KT + r < n;
-      uint4* dst = sk + r * CPR + (ck ^ (r & 7));
-      copy16(dst, on ? kp + key * x.ks : x.k, on);
-      copy16(dst + KT * CPR, on ? vp + key * x.vs : x.v, on);
+  for (int i = 0; i < TURN; ++i) to[i] = (rk + i * KPI) * ROW + (ck ^ ((rk + i * KPI) & 7)) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) from[i] = (lane & 15) * ROW + ((2 * i + (lane >> 4)) ^ (lane & 7)) * 16;
+  auto fetch = [&](uint32_t base) {
+    const char *ka = kp, *va = vp;
+    if (next < hi && next * KT + KT <= n) {
+#pragma unroll
+      for (int i = 0; i < KT / KPI; ++i, ka += kstep, va += vstep) {
+        const uint32_t dst = base + to[i % TURN] + i / TURN * 8 * ROW;
+        copy16(dst, ka);
+        copy16(dst + HALF, va);
+      }
+    } else if (next < hi) {  // the last stage: rows past the length are zeros
+#pragma unroll
+      for (int i = 0; i < KT / KPI; ++i, ka += kstep, va += vstep) {
+        const uint32_t dst = base + to[i % TURN] + i / TURN * 8 * ROW;
+        const bool on = next * KT + rk + i * KPI < n;
+        copy16(dst, on ? ka : reinterpret_cast<const char*>(x.k), on);
+        copy16(dst + HALF, on ? va : reinterpret_cast<const char*>(x.v), on);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    next += nw;
+    kp += nw * (KT / KPI) * kstep;
+    vp += nw * (KT / KPI) * vstep;
   };
-  int it = lo + warp;
 #pragma unroll
-  for (int s = 0; s < NS - 1; ++s) fetch(s, it + s * nw);
-  // the query rows as left operands: rows g and g + 8, columns t2 and t2 + 8 of every 16
-  uint32_t qa[D / 16][4];
+  for (int s = 0; s < NS - 1; ++s) fetch(mine + s * STAGE);
+  // the query rows as right operands: row g of a block, columns t2 and t2 + 8 of every 16
+  uint32_t qb[NB][D / 16][2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = g + 8 * h;
+  for (int nb = 0; nb < NB; ++nb) {
+    const int r = g + 8 * nb;
     const uint32_t* p = reinterpret_cast<const uint32_t*>(x.q + (((long long)b * x.Tq + r / x.G) * x.H + hk * x.G + r % x.G) * D + t2);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      qa[i][h] = r < x.rows ? __ldg(p + 8 * i) : 0u;
-      qa[i][h + 2] = r < x.rows ? __ldg(p + 8 * i + 4) : 0u;
+      qb[nb][i][0] = r < x.rows ? __ldg(p + 8 * i) : 0u;
+      qb[nb][i][1] = r < x.rows ? __ldg(p + 8 * i + 4) : 0u;
     }
   }
-  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // of rows t2 and t2 + 1 of a block: the output's columns, the reference (log2 units) and this lane's part of the sum
+  float o[NB][D / 16][4], m[NB][2], l[NB][2];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  for (int nb = 0; nb < NB; ++nb) {
+    m[nb][0] = m[nb][1] = -INFINITY;
+    l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
+  }
   const float c = x.scale * kLog2e;
-  int st = 0;
+  uint32_t sk = mine, fill = mine + (NS - 1) * STAGE;
 #pragma unroll 1
   for (; it < hi; it += nw) {
     __syncwarp();  // the stage filled next was read by every lane
-    fetch(st == 0 ? NS - 1 : st - 1, it + (NS - 1) * nw);
+    fetch(fill);
+    fill = fill == mine + (NS - 1) * STAGE ? mine : fill + STAGE;
     asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
     __syncwarp();
-    const uint4* sk = mine + st * stage_chunks<D>();
-    const uint4* sv = sk + KT * CPR;
-    st = st + 1 == NS ? 0 : st + 1;
-    // scores of states 0..7 and 8..15, two chains each
-    float s[2][2][4];
+    // scores of 16 states, two chains
+    float s[NB][2][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][0][e] = s[j][1][e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = 8 * j + (lane & 7);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t kb[4];
-        blocks4(kb, smem_addr(sk + r * CPR + ((4 * i + (lane >> 3)) ^ (r & 7))));
-        mma16(s[j][0], qa[2 * i], kb[0], kb[1]);
-        mma16(s[j][1], qa[2 * i + 1], kb[2], kb[3]);
-      }
-    }
-    uint32_t pa[4];
-    float f[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float z[4], mx = m[h];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = it * KT + 8 * (e >> 1) + t2 + (e & 1);
-        z[e] = (s[e >> 1][0][2 * h + (e & 1)] + s[e >> 1][1][2 * h + (e & 1)]) * c;
-        if (key >= n) z[e] = -INFINITY;
-        mx = fmaxf(mx, z[e]);
-      }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // no score above -inf so far: the reference stays at zero, weights of 0 and not of inf - inf
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      f[h] = ex2(m[h] - ref);
-      m[h] = mx;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[e] = ex2(z[e] - ref);
-      l[h] = fmaf(l[h], f[h], (z[0] + z[1]) + (z[2] + z[3]));
-      pa[h] = pack_bf16(z[0], z[1]);      // the product's operand type; l adds the unrounded weights
-      pa[h + 2] = pack_bf16(z[2], z[3]);
-    }
-    if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= f[0];
-        o[i][1] *= f[0];
-        o[i][2] *= f[1];
-        o[i][3] *= f[1];
-      }
-    }
-    const int r = lane & 15;
+      for (int e = 0; e < 4; ++e) s[nb][0][e] = s[nb][1][e] = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      uint32_t vb[4];
-      blocks4_t(vb, smem_addr(sv + r * CPR + ((2 * i + (lane >> 4)) ^ (r & 7))));
-      mma16(o[2 * i], pa, vb[0], vb[1]);
-      mma16(o[2 * i + 1], pa, vb[2], vb[3]);
+      uint32_t a[4];
+      blocks4(a, sk + from[i % 4] + i / 4 * 128);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) mma16(s[nb][i & 1], a, qb[nb][i][0], qb[nb][i][1]);
     }
+    bool above = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[nb][0][e] = (s[nb][0][e] + s[nb][1][e]) * c;
+        if (it * KT + KT > n && it * KT + g + 8 * (e >> 1) >= n) s[nb][0][e] = -INFINITY;
+        above |= s[nb][0][e] > m[nb][e & 1] + kSlack;
+      }
+    // The reference moves only once a score exceeds it by 2^8: weights up to 2^8 lose nothing, and the maximum over the
+    // lanes and the rescaling of the output stay out of most stages.
+    if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(s[nb][0][e], s[nb][0][e + 2]);
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          mx = fmaxf(mx, m[nb][e]);
+          f[e] = mx == -INFINITY ? 1.f : ex2(m[nb][e] - mx);
+          m[nb][e] = mx;
+          l[nb][e] *= f[e];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[nb][i][0] *= f[0];
+          o[nb][i][1] *= f[1];
+          o[nb][i][2] *= f[0];
+          o[nb][i][3] *= f[1];
+        }
+      }
+    }
+    uint32_t pb[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float z[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // no score above -inf so far: weights of 0 and not of inf - inf
+        const float ref = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
+        z[e] = ex2(s[nb][0][e] - ref);
+      }
+      l[nb][0] += z[0] + z[2];
+      l[nb][1] += z[1] + z[3];
+      pb[nb][0] = turned(pack_bf16(z[0], z[1]));  // the product's operand type; l adds the unrounded weights
+      pb[nb][1] = turned(pack_bf16(z[2], z[3]));
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t a[4];
+      blocks4_t(a, sk + HALF + from[i % 4] + i / 4 * 128);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) mma16(o[nb][i], a, pb[nb][0], pb[nb][1]);
+    }
+    sk = sk == mine + (NS - 1) * STAGE ? mine : sk + STAGE;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   // the warps' results in shared memory: [warp][rows][D + 2] = o, m, l; then the CTA's, [rows][D + 2] behind them
@@ -201,19 +250,25 @@ __global__ void __launch_bounds__(32 * most_warps<D>()) k_xattn_few(const XfDev 
   float* res = reinterpret_cast<float*>(ring);
   float* cta = res + nw * x.rows * RW;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    if (g + 8 * h < x.rows) {
-      float* p = res + (warp * x.rows + g + 8 * h) * RW;
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(p + 8 * i + t2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
-      if (t2 == 0) {
-        p[D] = m[h];
-        p[D + 1] = l[h];
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
+      const int r = 8 * nb + t2 + e;
+      if (r < x.rows) {
+        float* p = res + (warp * x.rows + r) * RW;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          p[16 * i + g] = o[nb][i][e];
+          p[16 * i + 8 + g] = o[nb][i][e + 2];
+        }
+        if (g == 0) {
+          p[D] = m[nb][e];
+          p[D + 1] = l[nb][e];
+        }
       }
     }
-  }
   __syncthreads();
   for (int i = threadIdx.x; i < x.rows * D; i += blockDim.x) {
     const int r = i / D, col = i % D;
@@ -264,7 +319,7 @@ __global__ void __launch_bounds__(32 * most_warps<D>()) k_xattn_few(const XfDev 
   cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
-template <int D>
+template <int D, int NB>
 cudaError_t launch(XfDev x, cudaStream_t s) {
   // A ring of 24 KB (d = 128) a warp: two CTAs of 4 warps on an SM, or one of 8.  The states are split over as many CTAs
   // as still run at once, while a warp has two stages or more.
@@ -275,7 +330,7 @@ cudaError_t launch(XfDev x, cudaStream_t s) {
   while (x.ns < kMaxCluster && base * 2 * x.ns <= 2 * 148 && stages >= 2 * x.ns * 2 * W) x.ns *= 2;
   const int warps = base * x.ns <= 148 ? 2 * W : W;
   static_assert(warp_smem<D>() >= 2 * ROWS * (D + 2) * sizeof(float), "the ring holds the warps' results and the CTA's");
-  const cudaError_t e = allow_smem<k_xattn_few<D>>(most_warps<D>() * warp_smem<D>());
+  const cudaError_t e = allow_smem<k_xattn_few<D, NB>>(most_warps<D>() * warp_smem<D>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(base * x.ns));
@@ -287,7 +342,7 @@ cudaError_t launch(XfDev x, cudaStream_t s) {
   at[0].val.clusterDim = {(unsigned)x.ns, 1, 1};
   lc.attrs = at;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, k_xattn_few<D>, x);
+  return cudaLaunchKernelEx(&lc, k_xattn_few<D, NB>, x);
 }
 
 }  // namespace
@@ -308,7 +363,8 @@ cudaError_t launch_xattn_few(const XDims& d, const XArgs& a, cudaStream_t s) {
   x.y = static_cast<__nv_bfloat16*>(const_cast<void*>(a.y));
   x.lse = a.lse;
   x.status = a.status;
-  return d.d == 128 ? launch<128>(x, s) : launch<64>(x, s);
+  if (x.rows > 8) return d.d == 128 ? launch<128, 2>(x, s) : launch<64, 2>(x, s);
+  return d.d == 128 ? launch<128, 1>(x, s) : launch<64, 1>(x, s);
 }
 
 }  // namespace vdn
