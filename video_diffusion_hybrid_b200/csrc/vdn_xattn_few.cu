@@ -322,13 +322,15 @@ __global__ void __launch_bounds__(32 * most_warps<D>()) k_xattn_few(const XfDev 
 template <int D, int NB>
 cudaError_t launch(XfDev x, cudaStream_t s) {
   // A ring of 24 KB (d = 128) a warp: two CTAs of 4 warps on an SM, or one of 8.  The states are split over as many CTAs
-  // as still run at once, while a warp has two stages or more.
+  // as still run at once, while a warp has two stages or more.  CTAs of 8 warps only up to 96 of them: a cluster of 8 needs
+  // 8 free SMs of one GPC then, and 16 clusters do not all fit at once (2 requests over 4,096 states: 16.0 us, with 4
+  // warps 12.1); 12 still do (11.0 us, with 4 warps 11.6), and one request takes 9.7 us (10.4).
   constexpr int W = most_warps<D>() / 2;
   const long long base = (long long)x.B * (x.H / x.G);
   const int stages = (x.L + KT - 1) / KT;
   x.ns = 1;
   while (x.ns < kMaxCluster && base * 2 * x.ns <= 2 * 148 && stages >= 2 * x.ns * 2 * W) x.ns *= 2;
-  const int warps = base * x.ns <= 148 ? 2 * W : W;
+  const int warps = base * x.ns <= 96 ? 2 * W : W;
   static_assert(warp_smem<D>() >= 2 * ROWS * (D + 2) * sizeof(float), "the ring holds the warps' results and the CTA's");
   const cudaError_t e = allow_smem<k_xattn_few<D, NB>>(most_warps<D>() * warp_smem<D>());
   if (e != cudaSuccess) return e;
