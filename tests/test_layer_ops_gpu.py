@@ -306,6 +306,32 @@ def test_cross_attn_rising_scores(cuda_ok, case):
     x_forward_check(op, q, k, v, n, dt, op(q, k, v, n))
 
 
+FEW = [  # few rows of a key head: one and two blocks of 8, full and not; lengths that end inside a stage of 16 states
+    (2, 4, 1100, 8, 2, 64, "bf16", [1100, 1089], True),
+    (1, 1, 2000, 16, 1, 128, "bf16", None, False),
+    (3, 3, 257, 6, 2, 128, "bf16", [257, 16, 0], True),
+    (2, 1, 4096, 9, 1, 64, "bf16", [4001, 15], True),
+    (40, 1, 65, 8, 8, 128, "bf16", [65 - i for i in range(40)], True),
+]
+
+
+@pytest.mark.parametrize("case", FEW, ids=str)
+def test_cross_attn_few_rows(cuda_ok, case):
+    op, q, k, v, n, clean, dt = x_case(case, 80)
+    x_forward_check(op, q, *clean, n, dt, op(q, k, v, n))
+
+
+@pytest.mark.parametrize("case", FEW, ids=str)
+@pytest.mark.parametrize("rise", [0.2, 0.7, 3.0, -3.0])
+def test_cross_attn_few_rows_rising_scores(cuda_ok, case, rise):
+    """The reference of the running sum follows only scores that leave it far behind: a rise that stays below that, one
+    that passes it now and then, one in nearly every stage, and a fall (weights that fade to zero)."""
+    op, q, k, v, n, _, dt = x_case(case, 81, poison=False)
+    q.fill_(1.0)
+    k.copy_(k * 0.1 + torch.linspace(-rise, rise, k.shape[1], device="cuda").view(1, -1, 1, 1))
+    x_forward_check(op, q, k, v, n, dt, op(q, k, v, n))
+
+
 @pytest.mark.parametrize("case", [X[1], X[9], X[-3]], ids=str)
 def test_cross_attn_states_that_weigh_nothing(cuda_ok, case):
     """States with a key of the type's lowest values: scores of -inf or close to it, a weight of zero."""
