@@ -283,6 +283,17 @@ vdn_status vdn_hybrid_device_status(const vdn_hybrid_cfg *cfg, const vdn_hybrid_
  * above the default limit), VDN_ERR_CUDA. */
 vdn_status vdn_debug_set_read_wait_limit(unsigned long long cycles);
 
+/* The same hook for the layer's operators (no counterpart on the pages): the
+ * limit, in SM clock cycles, of every bounded wait of the backward kernels of
+ * the cross-attention on the tensor cores (vdn_cross_attn_bwd), in the launches
+ * made from now on by this process; 0 restores the default.  A wait that runs
+ * out records VDN_ERR_TIMEOUT and the kernel's tag in the call's status words;
+ * the CTA then stops issuing, drains what it issued and exits with its outputs
+ * incomplete, and the context stays usable.  Host only: launches and captured
+ * graphs keep the limit that they were made with.  Errors: VDN_ERR_INVALID_ARG
+ * (cycles above the default limit). */
+vdn_status vdn_debug_set_layer_wait_limit(unsigned long long cycles);
+
 /* Which implementation a stage uses for cfg: 0 = SIMT fp32, 1 = tcgen05 tensor
  * cores (TMA + TMEM), 2 = the ablation variants' per-frame map kernel (SOLVE
  * with cfg.update != 0), -1 = stage not supported for cfg.  Also answers for

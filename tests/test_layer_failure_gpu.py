@@ -1,0 +1,66 @@
+"""The failure path of the layer's operators, made to happen without a fault:
+their bounded waits get a limit far below what a load or a product takes, so
+that some role of every CTA gives up.  The call's status words say so, the
+CTAs drain what they issued and end, and the next call of the same process,
+with the default limit, gives the same bits as before.  The limits put the
+give-up at different places: at the first loads, between two loads of an item,
+in the middle of the walk over the items.
+"""
+import pytest
+import torch
+
+from video_diffusion_hybrid_b200 import _lib as L
+from video_diffusion_hybrid_b200.api import CrossAttention
+from video_diffusion_hybrid_b200.build import build
+
+pytestmark = pytest.mark.gpu
+LIMITS = [1, 300, 1000, 3000, 10000]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if torch.cuda.is_available():
+        build()
+
+
+def attention(d):
+    """More items than SMs in every kernel, an empty batch element between full ones, a tile that ends early."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    B, Tq, Lk, H, Hkv = 3, 1500, 700, 12, 12
+    q, dy = (torch.randn(B, Tq, H, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    k, v = (torch.randn(B, Lk, Hkv, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    n = torch.tensor([700, 0, 300], device="cuda", dtype=torch.int32)
+    op = CrossAttention(B, Tq, Lk, H, Hkv, d, keep_lse=True)
+    assert (L.vdn_cross_attn_impl(op.cfg), L.vdn_cross_attn_impl(op.cfg, True)) == (1, 1)
+    return op, q, k, v, n, dy
+
+
+def gave_up(call, status, limits, tag):
+    """Runs `call` with each limit; the timeout is reported, under the kernel's tag, at the shortest at least."""
+    seen = []
+    torch.cuda.synchronize()
+    for cycles in limits:
+        L.vdn_debug_set_layer_wait_limit(cycles)
+        try:
+            call()
+            seen.append(status())
+            torch.cuda.synchronize()
+        finally:
+            L.vdn_debug_set_layer_wait_limit(0)
+        assert seen[-1] in ((L.VDN_OK, 0), (L.VDN_ERR_TIMEOUT, tag)), (cycles, seen)
+    assert seen[0][0] == L.VDN_ERR_TIMEOUT, seen
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_cross_attn_backward_wait_runs_out(cuda_ok, d):
+    op, q, k, v, n, dy = attention(d)
+    y = op(q, k, v, n)
+    lse = op.lse.clone()
+    back = lambda: op.backward(q, k, v, y, lse, dy, n)  # noqa: E731
+    want = back()
+    assert op.status(backward=True) == (L.VDN_OK, 0)
+    for _ in range(3):
+        gave_up(back, lambda: op.status(backward=True), LIMITS, L.TAG_XATTN_BWD)
+        got = back()
+        assert op.status(backward=True) == (L.VDN_OK, 0)
+        assert all(torch.equal(want[key], got[key]) for key in want)

@@ -216,3 +216,10 @@ def test_int8_workspace_is_for_codes_and_scales():
     assert L.vdn_linear_int8_workspace_size(i8_cfg(M=8)) == 0
     assert L.vdn_linear_int8_workspace_size(i8_cfg(M=9)) >= 9 * 64 + 9 * 4
     assert L.vdn_linear_int8_workspace_size(i8_cfg(M=1 << 20, K=131056)) >= (1 << 20) * (131056 + 4)
+
+
+def test_layer_wait_limit_is_bounded():
+    """The failure tests' hook: up to the default limit of about a second, and no further."""
+    assert L.vdn_debug_set_layer_wait_limit(2_000_000_001, check=False) == L.VDN_ERR_INVALID_ARG
+    assert L.vdn_debug_set_layer_wait_limit(300) == L.VDN_OK
+    assert L.vdn_debug_set_layer_wait_limit(0) == L.VDN_OK

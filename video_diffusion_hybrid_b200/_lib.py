@@ -27,7 +27,7 @@ EXPORTED = ("vdn_hybrid_attn_workspace_size", "vdn_hybrid_workspace_layout", "vd
             "vdn_status_string", "vdn_hybrid_attn_fwd_noalloc", "vdn_hybrid_noalloc_device_status", "vdn_out_proj", "vdn_text_cross_attn",
             "vdn_quantize_fp8", "vdn_out_proj_fp8", "vdn_hybrid_lin_bwd_workspace_size", "vdn_hybrid_lin_bwd",
             "vdn_hybrid_sm_bwd_workspace_size", "vdn_hybrid_sm_bwd", "vdn_hybrid_bwd_workspace_size", "vdn_hybrid_bwd",
-            "vdn_debug_set_read_wait_limit", "vdn_proj_device_status",
+            "vdn_debug_set_read_wait_limit", "vdn_debug_set_layer_wait_limit", "vdn_proj_device_status",
             "vdn_qk_norm_rope", "vdn_qk_norm_rope_bwd", "vdn_qk_norm_rope_bwd_workspace_size",
             "vdn_cross_attn", "vdn_cross_attn_bwd", "vdn_cross_attn_workspace_size",
             "vdn_cross_attn_bwd_workspace_size", "vdn_cross_attn_impl", "vdn_cross_attn_device_status",
@@ -221,6 +221,8 @@ def lib() -> C.CDLL:
         L.vdn_proj_device_status.argtypes = [C.c_void_p, C.POINTER(C.c_uint)]
         L.vdn_debug_set_read_wait_limit.restype = C.c_int
         L.vdn_debug_set_read_wait_limit.argtypes = [C.c_ulonglong]
+        L.vdn_debug_set_layer_wait_limit.restype = C.c_int
+        L.vdn_debug_set_layer_wait_limit.argtypes = [C.c_ulonglong]
         for name, types in (("vdn_qk_norm_rope", (QkCfg, QkArgs)), ("vdn_qk_norm_rope_bwd", (QkCfg, QkArgs, QkGrads)),
                             ("vdn_cross_attn", (XattnCfg, XattnArgs)),
                             ("vdn_cross_attn_bwd", (XattnCfg, XattnArgs, XattnGrads)),
@@ -443,6 +445,7 @@ def vdn_hybrid_bwd(cfg: HybridCfg, args: VdnArgs, grads: VdnGrads, stream=None, 
 
 
 TAG_READ = 3  # VDN_TAG_READ
+TAG_XATTN, TAG_XATTN_BWD = 9, 10  # VDN_TAG_XATTN, VDN_TAG_XATTN_BWD
 
 
 def vdn_debug_set_read_wait_limit(cycles: int, check: bool = True) -> int:
@@ -452,6 +455,12 @@ def vdn_debug_set_read_wait_limit(cycles: int, check: bool = True) -> int:
     if check and st != VDN_OK:
         raise VdnError(st, "vdn_debug_set_read_wait_limit")
     return st
+
+
+def vdn_debug_set_layer_wait_limit(cycles: int, check: bool = True) -> int:
+    """Wait limit (SM clock cycles) of the layer operators' kernels in the
+    launches from now on; 0 = the default.  Failure-path tests only."""
+    return _checked(lib().vdn_debug_set_layer_wait_limit(int(cycles)), "vdn_debug_set_layer_wait_limit", check)
 
 
 def vdn_proj_device_status(stream=None) -> tuple:

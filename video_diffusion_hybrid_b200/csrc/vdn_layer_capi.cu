@@ -2,6 +2,7 @@
 // rotation of queries and keys, cross-attention with lengths, the 8-bit
 // integer linear layer.  Argument validation and dispatch; the kernels are in
 // vdn_qk_rope.cu, vdn_xattn*.cu, vdn_int8.cu and vdn_gemm_tc.cu.
+#include <atomic>
 #include <cstdint>
 
 #include "vdn_xattn.h"
@@ -11,6 +12,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr long long kMax31 = 1LL << 31;
+constexpr unsigned long long kMostWaitCycles = 2000000000ULL;  // the default limit of a bounded wait
 size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool ok_ptr(const void* p, size_t a) { return p != nullptr && aligned(p, a); }
@@ -86,6 +88,9 @@ vdn_status check_x_args(const vdn_xattn_cfg* c, const vdn_xattn_args* a, size_t 
   return VDN_OK;
 }
 
+// set by vdn_debug_set_layer_wait_limit, read at every launch
+std::atomic<long long> g_wait_limit{0};
+
 XArgs xargs(const vdn_xattn_args* a, const vdn_xattn_grads* g) {
   XArgs x{};
   x.q = a->q; x.k = a->k; x.v = a->v; x.y = a->y; x.lse = a->lse;
@@ -94,6 +99,7 @@ XArgs xargs(const vdn_xattn_args* a, const vdn_xattn_grads* g) {
   }
   x.status = static_cast<uint32_t*>(a->workspace);
   x.scratch = static_cast<char*>(a->workspace) + kAlign;
+  x.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   return x;
 }
 
@@ -196,6 +202,12 @@ vdn_status vdn_cross_attn_device_status(const void* workspace, vdn_stream_t stre
   if (cudaStreamSynchronize(s) != cudaSuccess) return VDN_ERR_CUDA;
   if (where) *where = host[1];
   return host[0] ? VDN_ERR_TIMEOUT : VDN_OK;
+}
+
+vdn_status vdn_debug_set_layer_wait_limit(unsigned long long cycles) {
+  if (cycles > kMostWaitCycles) return VDN_ERR_INVALID_ARG;
+  g_wait_limit.store((long long)cycles, std::memory_order_relaxed);
+  return VDN_OK;
 }
 
 vdn_status vdn_quantize_int8(const void* x, int x_dtype, int rows, int cols, void* q, float* scale, vdn_stream_t stream) {

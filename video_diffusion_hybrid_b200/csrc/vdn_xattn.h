@@ -21,6 +21,7 @@ struct XArgs {
   void *dq, *dk, *dv;
   uint32_t* status;    // status words of the bounded waits; a call's first kernel clears them
   void* scratch;       // backward: behind the status words
+  long long wait_limit;  // of the tensor-core kernels' bounded waits, in clock cycles; 0: the default
 };
 
 __device__ __forceinline__ int kv_valid(const XDims& d, int b) {

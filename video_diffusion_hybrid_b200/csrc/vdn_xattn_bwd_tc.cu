@@ -61,6 +61,7 @@ struct XbDev {
   __nv_bfloat16 *dq, *dk, *dv;
   float *part, *part2;      // partial sums: dq [ns][B Tq H][D], or dk and dv [ns][B L Hkv][D]; null: none
   uint32_t* status;
+  long long wait_limit;     // of the bounded waits, in clock cycles; 0: the default
 };
 
 __device__ __forceinline__ int valid_states(const XbDev& x, int b) {
@@ -214,7 +215,7 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Ctl ctl{abort_flag, x.status, (unsigned)VDN_TAG_XATTN_BWD, 0};
+  const Ctl ctl{abort_flag, x.status, (unsigned)VDN_TAG_XATTN_BWD, x.wait_limit};
   auto bar = [&](int i) { return smem_u32(bars + i); };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i == B_DS || i == B_STEMPTY ? kSoftWarps : 1);
@@ -229,8 +230,10 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
 
   if (warp == 0) {
     // ---- producer: Q and dO of an item (dO once its first V is under way), the K and V rings
+    // Loads issued, each counted at its own place and before the next wait: after a give-up the counts are what there is to
+    // drain (a Q counted only behind the wait for K's stage could still be on its way into a CTA that has ended).
     QWalk w;
-    int ni = 0, nk = 0;  // loads issued
+    int nq = 0, no = 0, nk = 0, nv = 0;
     for (w.start(x); w.on; w.next(x)) {
       bool ok = true;
       if (lane == 0) {
@@ -239,6 +242,7 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
           if (ok) {
             mbar_expect_tx(bar(B_QFULL), TILE);
             for (int c = 0; c < NB; ++c) tma_load_4d(smem_u32(sQ + c * BR * 128), &tmq, bar(B_QFULL), c * 64, w.it.h, w.it.q0, w.it.b);
+            nq = w.i + 1;
           }
         }
         const int sk = w.n % KST, sv = w.n % VST;
@@ -249,11 +253,11 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
             tma_load_3d(smem_u32(sK + sk * TILE + c * BR * 128), &tmk, bar(B_KFULL + sk), c * 64, w.it.h / x.G, w.it.k0 + w.j * BR);
           nk = w.n + 1;
           if (w.j == 0) {
-            ni = w.i + 1;
             ok = w.i == 0 || mbar_wait(bar(B_OEMPTY), (w.i - 1) & 1, ctl);
             if (ok) {
               mbar_expect_tx(bar(B_OFULL), TILE);
               for (int c = 0; c < NB; ++c) tma_load_4d(smem_u32(sO + c * BR * 128), &tmdo, bar(B_OFULL), c * 64, w.it.h, w.it.q0, w.it.b);
+              no = w.i + 1;
             }
           }
           ok = ok && (w.n < VST || mbar_wait(bar(B_VEMPTY + sv), (w.n / VST - 1) & 1, ctl));
@@ -261,6 +265,7 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
             mbar_expect_tx(bar(B_VFULL + sv), TILE);
             for (int c = 0; c < NB; ++c)
               tma_load_3d(smem_u32(sV + sv * TILE + c * BR * 128), &tmv, bar(B_VFULL + sv), c * 64, w.it.h / x.G, w.it.k0 + w.j * BR);
+            nv = w.n + 1;
           }
         }
       }
@@ -278,11 +283,11 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
       }
     }
     if (lane == 0) {
-      // what was issued has landed (after a give-up a wait on a load that was not issued runs out, bounded)
-      if (ni > 0) mbar_drain(bar(B_QFULL), (ni - 1) & 1);
-      if (ni > 0) mbar_drain(bar(B_OFULL), (ni - 1) & 1);
+      // what was issued has landed
+      if (nq > 0) mbar_drain(bar(B_QFULL), (nq - 1) & 1);
+      if (no > 0) mbar_drain(bar(B_OFULL), (no - 1) & 1);
       for (int n = max(nk - KST, 0); n < nk; ++n) mbar_drain(bar(B_KFULL + n % KST), (n / KST) & 1);
-      for (int n = max(nk - VST, 0); n < nk; ++n) mbar_drain(bar(B_VFULL + n % VST), (n / VST) & 1);
+      for (int n = max(nv - VST, 0); n < nv; ++n) mbar_drain(bar(B_VFULL + n % VST), (n / VST) & 1);
     }
   } else if (warp == 1) {
     // ---- MMA issuer (the whole warp, converged; one elected lane issues)
@@ -542,7 +547,7 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
   }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Ctl ctl{abort_flag, x.status, (unsigned)VDN_TAG_XATTN_BWD, 0};
+  const Ctl ctl{abort_flag, x.status, (unsigned)VDN_TAG_XATTN_BWD, x.wait_limit};
   auto bar = [&](int i) { return smem_u32(bars + i); };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBARS; ++i)
@@ -559,7 +564,7 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
   if (warp == 0) {
     // ---- producer: K and V of an item, the Q and dO rings
     KWalk w;
-    int ni = 0, nq = 0;
+    int nk = 0, nq = 0, nv = 0, no = 0;  // loads issued, counted as in dq's producer
     for (w.start(x); w.on; w.next(x)) {
       const int sq = w.n % QST, so = w.n % OST, h = w.head(x), t0 = w.tok();
       if (w.j == 0) {
@@ -569,7 +574,7 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
           for (int c = 0; c < NB; ++c)
             tma_load_3d(smem_u32(sK + c * BR * 128), &tmk, bar(B_KFULL), c * 64, w.it.hk, w.it.b * x.L + w.it.k0);
         }
-        ni = w.i + 1;
+        nk = w.i + 1;
       }
       if (w.n >= QST && !mbar_wait_warp(bar(B_QEMPTY + sq), (w.n / QST - 1) & 1, ctl)) break;
       if (lane == 0) {
@@ -585,6 +590,7 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
           for (int c = 0; c < NB; ++c)
             tma_load_3d(smem_u32(sV + c * BR * 128), &tmv, bar(B_VFULL), c * 64, w.it.hk, w.it.b * x.L + w.it.k0);
         }
+        nv = w.i + 1;
       }
       if (w.n >= OST && !mbar_wait_warp(bar(B_OEMPTY + so), (w.n / OST - 1) & 1, ctl)) break;
       if (lane == 0) {
@@ -592,12 +598,13 @@ k_xattn_dkv_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __g
         for (int c = 0; c < NB; ++c)
           tma_load_4d(smem_u32(sO + so * TILE + c * BR * 128), &tmdo, bar(B_OFULL + so), c * 64, h, t0, w.it.b);
       }
+      no = w.n + 1;
     }
     if (lane == 0) {
-      if (ni > 0) mbar_drain(bar(B_KFULL), (ni - 1) & 1);
-      if (ni > 0) mbar_drain(bar(B_VFULL), (ni - 1) & 1);
+      if (nk > 0) mbar_drain(bar(B_KFULL), (nk - 1) & 1);
+      if (nv > 0) mbar_drain(bar(B_VFULL), (nv - 1) & 1);
       for (int n = max(nq - QST, 0); n < nq; ++n) mbar_drain(bar(B_QFULL + n % QST), (n / QST) & 1);
-      for (int n = max(nq - OST, 0); n < nq; ++n) mbar_drain(bar(B_OFULL + n % OST), (n / OST) & 1);
+      for (int n = max(no - OST, 0); n < no; ++n) mbar_drain(bar(B_OFULL + n % OST), (n / OST) & 1);
     }
   } else if (warp == 1) {
     // ---- MMA issuer
@@ -919,6 +926,7 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
   x.dk = static_cast<__nv_bfloat16*>(a.dk);
   x.dv = static_cast<__nv_bfloat16*>(a.dv);
   x.status = a.status;
+  x.wait_limit = a.wait_limit;
   const long long qi = (long long)d.B * d.H * c.nqt * c.qs, ki = (long long)d.B * d.Hkv * c.nkt * c.ks;
   if (qi > 0x7FFFFFFFLL || ki > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const size_t smq = 1024 + (size_t)7 * BR * D * 2 + BR * sizeof(float2) + 32 * 8 + 16, smk = dkv_smem<D>();
