@@ -235,45 +235,40 @@ k_xattn_dq_tc(const XbDev x, const __grid_constant__ CUtensorMap tmq, const __gr
     QWalk w;
     int nq = 0, no = 0, nk = 0, nv = 0;
     for (w.start(x); w.on; w.next(x)) {
-      bool ok = true;
-      if (lane == 0) {
-        if (w.j == 0) {
-          ok = w.i == 0 || mbar_wait(bar(B_QEMPTY), (w.i - 1) & 1, ctl);
-          if (ok) {
-            mbar_expect_tx(bar(B_QFULL), TILE);
-            for (int c = 0; c < NB; ++c) tma_load_4d(smem_u32(sQ + c * BR * 128), &tmq, bar(B_QFULL), c * 64, w.it.h, w.it.q0, w.it.b);
-            nq = w.i + 1;
-          }
+      const int sk = w.n % KST, sv = w.n % VST;
+      if (w.j == 0) {
+        if (w.i > 0 && !mbar_wait_warp(bar(B_QEMPTY), (w.i - 1) & 1, ctl)) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(B_QFULL), TILE);
+          for (int c = 0; c < NB; ++c) tma_load_4d(smem_u32(sQ + c * BR * 128), &tmq, bar(B_QFULL), c * 64, w.it.h, w.it.q0, w.it.b);
         }
-        const int sk = w.n % KST, sv = w.n % VST;
-        ok = ok && (w.n < KST || mbar_wait(bar(B_KEMPTY + sk), (w.n / KST - 1) & 1, ctl));
-        if (ok) {
-          mbar_expect_tx(bar(B_KFULL + sk), TILE);
-          for (int c = 0; c < NB; ++c)
-            tma_load_3d(smem_u32(sK + sk * TILE + c * BR * 128), &tmk, bar(B_KFULL + sk), c * 64, w.it.h / x.G, w.it.k0 + w.j * BR);
-          nk = w.n + 1;
-          if (w.j == 0) {
-            ok = w.i == 0 || mbar_wait(bar(B_OEMPTY), (w.i - 1) & 1, ctl);
-            if (ok) {
-              mbar_expect_tx(bar(B_OFULL), TILE);
-              for (int c = 0; c < NB; ++c) tma_load_4d(smem_u32(sO + c * BR * 128), &tmdo, bar(B_OFULL), c * 64, w.it.h, w.it.q0, w.it.b);
-              no = w.i + 1;
-            }
-          }
-          ok = ok && (w.n < VST || mbar_wait(bar(B_VEMPTY + sv), (w.n / VST - 1) & 1, ctl));
-          if (ok) {
-            mbar_expect_tx(bar(B_VFULL + sv), TILE);
-            for (int c = 0; c < NB; ++c)
-              tma_load_3d(smem_u32(sV + sv * TILE + c * BR * 128), &tmv, bar(B_VFULL + sv), c * 64, w.it.h / x.G, w.it.k0 + w.j * BR);
-            nv = w.n + 1;
-          }
-        }
+        nq = w.i + 1;
       }
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (w.n >= KST && !mbar_wait_warp(bar(B_KEMPTY + sk), (w.n / KST - 1) & 1, ctl)) break;
+      if (lane == 0) {
+        mbar_expect_tx(bar(B_KFULL + sk), TILE);
+        for (int c = 0; c < NB; ++c)
+          tma_load_3d(smem_u32(sK + sk * TILE + c * BR * 128), &tmk, bar(B_KFULL + sk), c * 64, w.it.h / x.G, w.it.k0 + w.j * BR);
+      }
+      nk = w.n + 1;
+      if (w.j == 0) {
+        if (w.i > 0 && !mbar_wait_warp(bar(B_OEMPTY), (w.i - 1) & 1, ctl)) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(B_OFULL), TILE);
+          for (int c = 0; c < NB; ++c) tma_load_4d(smem_u32(sO + c * BR * 128), &tmdo, bar(B_OFULL), c * 64, w.it.h, w.it.q0, w.it.b);
+        }
+        no = w.i + 1;
+      }
+      if (w.n >= VST && !mbar_wait_warp(bar(B_VEMPTY + sv), (w.n / VST - 1) & 1, ctl)) break;
+      if (lane == 0) {
+        mbar_expect_tx(bar(B_VFULL + sv), TILE);
+        for (int c = 0; c < NB; ++c)
+          tma_load_3d(smem_u32(sV + sv * TILE + c * BR * 128), &tmv, bar(B_VFULL + sv), c * 64, w.it.h / x.G, w.it.k0 + w.j * BR);
+      }
+      nv = w.n + 1;
       const int valid = w.it.nk - w.j * BR;
       if (valid < BR) {  // rows of K past the last state: zeros
-        const int sk = w.n % KST;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_KFULL + sk), (w.n / KST) & 1, ctl))) break;
+        if (!mbar_wait_warp(bar(B_KFULL + sk), (w.n / KST) & 1, ctl)) break;
         for (int c = 0; c < NB; ++c) {
           uint4* base = reinterpret_cast<uint4*>(sK + sk * TILE + c * BR * 128);
           for (int i = valid * 8 + lane; i < BR * 8; i += 32) base[i] = make_uint4(0, 0, 0, 0);
