@@ -284,9 +284,9 @@ vdn_status vdn_hybrid_device_status(const vdn_hybrid_cfg *cfg, const vdn_hybrid_
 vdn_status vdn_debug_set_read_wait_limit(unsigned long long cycles);
 
 /* The same hook for the layer's operators (no counterpart on the pages): the
- * limit, in SM clock cycles, of every bounded wait of the backward kernels of
- * the cross-attention on the tensor cores (vdn_cross_attn_bwd), in the launches
- * made from now on by this process; 0 restores the default.  A wait that runs
+ * limit, in SM clock cycles, of every bounded wait of the cross-attention's
+ * kernels on the tensor cores (vdn_cross_attn, vdn_cross_attn_bwd), in the
+ * launches made from now on by this process; 0 restores the default.  A wait that runs
  * out records VDN_ERR_TIMEOUT and the kernel's tag in the call's status words;
  * the CTA then stops issuing, drains what it issued and exits with its outputs
  * incomplete, and the context stays usable.  Host only: launches and captured

@@ -64,3 +64,15 @@ def test_cross_attn_backward_wait_runs_out(cuda_ok, d):
         got = back()
         assert op.status(backward=True) == (L.VDN_OK, 0)
         assert all(torch.equal(want[key], got[key]) for key in want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_cross_attn_wait_runs_out(cuda_ok, d):
+    op, q, k, v, n, _ = attention(d)
+    want = op(q, k, v, n)
+    lse = op.lse.clone()
+    assert op.status() == (L.VDN_OK, 0)
+    for _ in range(3):
+        gave_up(lambda: op(q, k, v, n), op.status, LIMITS, L.TAG_XATTN)
+        assert torch.equal(want, op(q, k, v, n)) and torch.equal(lse, op.lse)
+        assert op.status() == (L.VDN_OK, 0)

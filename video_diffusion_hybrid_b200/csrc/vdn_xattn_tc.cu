@@ -70,6 +70,7 @@ struct XtDev {
   float *po, *pl;      // partial outputs [parts][B Tq H][D] and log-sum-exps (log2 units), or null
   long long rows;      // B Tq H
   uint32_t* status;
+  long long wait_limit;  // of the bounded waits, in clock cycles; 0: the default
 };
 
 struct Item {
@@ -156,7 +157,7 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Ctl ctl{abort_flag, x.status, (unsigned)VDN_TAG_XATTN, 0};
+  const Ctl ctl{abort_flag, x.status, (unsigned)VDN_TAG_XATTN, x.wait_limit};
   auto bar = [&](int i) { return smem_u32(bars + i); };
 
   clear_status(x.status);
@@ -288,6 +289,7 @@ k_xattn_tc(const XtDev x, const __grid_constant__ CUtensorMap tmq, const __grid_
           if (t == 0)  // V of this key tile
             ok = mbar_wait_warp(bar(B_VFULL + sv), (w.n / VST) & 1, ctl) &&
                  (!part || mbar_wait_warp(bar(B_VFIX + sv), (fixes >> sv) & 1, ctl));
+          if (!ok) break;  // not lost to the waits below: no product on a V that is not there, or not zeroed
           // O_t += P_t V in two halves of 64 states, the first one while the softmax forms the second
           const uint64_t vd = dadd(vd0, sv * KVBYTES);
           const uint32_t dst = tmem + col_o(t), pa = tmem + col_s(t);
@@ -597,6 +599,7 @@ cudaError_t launch(const XDims& d, const XArgs& a, cudaStream_t s) {
     x.pl = x.po + (long long)c.parts * x.rows * D;
   }
   x.status = a.status;
+  x.wait_limit = a.wait_limit;
   const size_t smem = 1024 + (size_t)2 * BM * D * 2 + (size_t)(KST + VST) * BN * D * 2 + 40 * 8 + 16;
   cudaError_t e = allow_smem<k_xattn_tc<D>>(smem);
   if (e != cudaSuccess) return e;
