@@ -1,0 +1,148 @@
+"""The layer's operators where their kernels change regime: several items of a
+persistent kernel on one SM, every tile shape of the 8-bit product, rows past
+2^31 elements."""
+import pytest
+import torch
+
+from oracle import layer_oracle as R
+from test_layer_ops_gpu import DT, QK, gen, qk_case, rnd, within, x_case, x_forward_check, x_grads, x_status
+from video_diffusion_hybrid_b200 import _lib as L
+from video_diffusion_hybrid_b200.api import CrossAttention, Int8Linear, quantize_int8, rope_table
+from video_diffusion_hybrid_b200.build import build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if torch.cuda.is_available():
+        build()
+
+
+def room_for(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gigabytes << 30:
+        pytest.skip(f"needs {gigabytes} GB")
+
+
+# ------------------------------------------------------- norm and rotation
+
+
+@pytest.mark.parametrize("gdtype", ["f32", "bf16"])
+def test_qk_backward_of_index_positions_and_unit_weights(cuda_ok, gdtype):
+    for case in (QK[3], QK[2]):
+        if case[7] == "f32" and gdtype == "bf16":
+            continue
+        op, a, _, dt = qk_case((case[0], *case[1:5], (case[4] // 2,), *case[6:]), 8, skip=False)
+        table = rope_table(case[0] + 3, (case[4] // 2,))
+        g = gen(9)
+        up = {k: rnd(g, *a[k].shape, dtype=DT[gdtype]) for k in "qk"}
+        got = op.backward(a["q"], a["k"], None, None, table, up["q"], up["k"])
+        p = torch.arange(case[0], device="cuda", dtype=torch.int32).unsqueeze(1)
+        for k in "qk":
+            dx, dw, scale, terms = R.qk_norm_rope_bwd(a[k], None, table, p, op.rot, case[6], op.sections, 1e-6, up[k])
+            within(got["d" + k], dx, R.step(dt) * dx.abs() + 64 * R.EPS * scale, "d" + k)
+            if not op.per_head:
+                dw, terms = dw.sum(0), terms.sum(0)
+            n = case[0] * (1 if op.per_head else a[k].shape[1])
+            within(got["dw" + k], dw, (n + 64) * R.EPS * terms + 1e-30, "dw" + k)
+
+
+# --------------------------------------------------------- cross-attention
+WIDE = [  # more items than SMs, so that a CTA goes on from one to the next: in the forward and dq, and mostly in dk and dv
+    (3, 1500, 700, 24, 24, 64, "bf16", [700, 0, 300], True),
+    (3, 1500, 700, 24, 8, 128, "bf16", [300, 700, 0], True),
+    (4, 1700, 515, 30, 10, 64, "bf16", [515, 0, 129, 1], False),   # heads of a group share tiles of 126 rows
+    (5, 1100, 260, 24, 24, 128, "bf16", [0, 260, 0, 128, 7], True),  # empty batch elements between
+    (2, 100, 8192, 40, 40, 64, "bf16", [8192, 3001], False),       # states split, more than one item a CTA
+    (2, 256, 8192, 40, 20, 128, "bf16", [3000, 8191], True),
+    (2, 6000, 600, 20, 10, 64, "bf16", [600, 385], False),         # query rows split in dk and dv
+    (2, 6000, 600, 20, 10, 128, "bf16", [511, 600], True),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=str)
+def test_cross_attn_many_items(cuda_ok, case):
+    op, q, k, v, n, clean, dt = x_case(case, 90)
+    assert L.vdn_cross_attn_impl(op.cfg) == 1
+    y = op(q, k, v, n)
+    x_status(op)
+    x_forward_check(op, q, *clean, n, dt, y)
+    assert all(torch.equal(y, op(q, k, v, n)) for _ in range(3))
+
+
+@pytest.mark.parametrize("case", WIDE, ids=str)
+def test_cross_attn_backward_many_items(cuda_ok, case):
+    op, q, k, v, n, clean, dt = x_case(case, 91)
+    assert L.vdn_cross_attn_impl(op.cfg, True) == 1
+    got = x_grads(op, q, k, v, n, clean, dt, 92)
+    for b, m in enumerate(case[7]):
+        assert bool((got["dk"][b, m:] == 0).all()) and bool((got["dv"][b, m:] == 0).all())
+        assert m > 0 or bool((got["dq"][b] == 0).all())
+
+
+def test_cross_attn_backward_offsets_past_31_bits(cuda_ok):
+    """More than 2^31 elements of q: the last rows' dq like that of the rows alone; the other rows have no gradient, so dk
+    and dv are the last rows' too, up to the order of their sums (a step of bf16 in the 2-norm)."""
+    room_for(60)
+    g, T, last = gen(52), (2 ** 31 + 2 ** 20) // (24 * 128), 700
+    q, dy = (torch.zeros(1, T, 24, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q[:, -last:], dy[:, -last:] = (rnd(g, 1, last, 24, 128, dtype=torch.bfloat16) for _ in range(2))
+    k, v = (rnd(g, 1, 200, 24, 128, dtype=torch.bfloat16) for _ in range(2))
+    big, few = CrossAttention(1, T, 200, 24, 24, 128, keep_lse=True), CrossAttention(1, last, 200, 24, 24, 128, keep_lse=True)
+    y = big(q, k, v)
+    a = big.backward(q, k, v, y, big.lse, dy)
+    qt, yt, dt = (t[:, -last:].contiguous() for t in (q, y, dy))
+    assert torch.equal(few(qt, k, v), yt)
+    b = few.backward(qt, k, v, yt, few.lse, dt)
+    assert torch.equal(a["dq"][:, -last:], b["dq"]) and bool((a["dq"][:, :1000] == 0).all())
+    for key in ("dk", "dv"):
+        x, z = a[key].double(), b[key].double()
+        assert float((x - z).norm()) <= 2 ** -8 * float(z.norm()), key
+
+
+# ------------------------------------------------------------ 8-bit layer
+TILES = [  # the CTA-pair kernel with more tiles than pairs, with fewer; 128 x 64 tiles; 128 x 32 tiles, several
+    (5000, 208, 1040), (4999, 6160, 1040), (20000, 48, 272), (1000, 1296, 784), (700, 272, 2000), (1008, 6144, 1024), (300, 144, 1040),
+    (513, 400, 512),
+]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "i8"])
+@pytest.mark.parametrize("M,K,N", TILES, ids=str)
+def test_linear_int8_tiles(cuda_ok, M, K, N, dtype, out):
+    g = gen(24)
+    w, ws = quantize_int8(rnd(g, N, K, scale=K ** -0.5))
+    bias = rnd(g, N) if M % 2 else None
+    op = Int8Linear(w, ws, bias, out_dtype=out)
+    room = torch.full((M * N + 256,), 7.0, device="cuda", dtype=DT[out])
+    y = room[:M * N].view(M, N)
+    if dtype == "i8":
+        codes = torch.randint(-128, 128, (M, K), device="cuda", generator=g, dtype=torch.int8)
+        xs = torch.rand(M, device="cuda", generator=g) + 0.1
+        op(codes, xs, out=y)
+    else:
+        x = rnd(g, M, K, dtype=DT[dtype])
+        codes, xs = R.quantize_int8(x)
+        op(x, out=y)
+    assert L.vdn_proj_device_status()[0] == L.VDN_OK
+    want = R.linear_int8(codes, xs, w, ws, bias)
+    size = want.abs() + (0 if bias is None else 2 * bias.abs())
+    within(y, want, (R.step(DT[out]) + 8 * R.EPS) * size, "out")
+    assert bool((room[M * N:] == 7.0).all())
+
+
+def test_linear_int8_offsets_past_31_bits(cuda_ok):
+    """More than 2^31 elements of x and of the output: the last rows like those rows alone."""
+    room_for(40)
+    g, M, K, last = gen(53), 360000, 6144, 300
+    w, ws = quantize_int8(rnd(g, K, K, scale=K ** -0.5))
+    op = Int8Linear(w, ws)
+    x = torch.zeros(M, K, device="cuda", dtype=torch.bfloat16)
+    x[-last:] = rnd(g, last, K, dtype=torch.bfloat16)
+    y = op(x)
+    assert torch.equal(y[-last:], op(x[-last:])) and bool((y[:1000] == 0).all())
+    q, s = quantize_int8(x)
+    qt, st = quantize_int8(x[-last:])
+    assert torch.equal(q[-last:], qt) and torch.equal(s[-last:], st)
