@@ -1,13 +1,16 @@
 """The layer's operators where their kernels change regime: several items of a
 persistent kernel on one SM, every tile shape of the 8-bit product, rows past
-2^31 elements."""
+2^31 elements, sizes next to 2^31, and what a call leaves in rows that it has
+nothing to compute for."""
+import math
+
 import pytest
 import torch
 
 from oracle import layer_oracle as R
-from test_layer_ops_gpu import DT, QK, gen, qk_case, rnd, within, x_case, x_forward_check, x_grads, x_status
+from test_layer_ops_gpu import DT, QK, X, gen, qk_case, rnd, within, x_case, x_forward_check, x_grads, x_status
 from video_diffusion_hybrid_b200 import _lib as L
-from video_diffusion_hybrid_b200.api import CrossAttention, Int8Linear, quantize_int8, rope_table
+from video_diffusion_hybrid_b200.api import CrossAttention, Int8Linear, QKNormRope, quantize_int8, rope_table
 from video_diffusion_hybrid_b200.build import build
 
 pytestmark = pytest.mark.gpu
@@ -79,6 +82,21 @@ def test_cross_attn_backward_many_items(cuda_ok, case):
     for b, m in enumerate(case[7]):
         assert bool((got["dk"][b, m:] == 0).all()) and bool((got["dv"][b, m:] == 0).all())
         assert m > 0 or bool((got["dq"][b] == 0).all())
+
+
+@pytest.mark.parametrize("case", [X[9], X[3], X[-3], X[-1], X[13]], ids=str)
+def test_cross_attn_no_gradient_past_the_length_of_a_bad_row(cuda_ok, case):
+    """A NaN or an infinity in the incoming gradient reaches the states of its batch element, not those past the length."""
+    op, q, k, v, n, _, dt = x_case(case, 93)
+    dy = rnd(gen(94), *q.shape, dtype=dt)
+    dy[:, 0, 0, 3], dy[:, -1, -1, 1] = math.nan, math.inf
+    y = op(q, k, v, n)
+    got = op.backward(q, k, v, y, op.lse, dy, n)
+    for b, m in enumerate(case[7]):
+        m = min(max(m, 0), k.shape[1])
+        for key in ("dk", "dv"):
+            assert bool((got[key][b, m:] == 0).all()), (key, b)
+            assert m == 0 or not bool(torch.isfinite(got[key][b, :m]).all())
 
 
 def test_cross_attn_backward_offsets_past_31_bits(cuda_ok):

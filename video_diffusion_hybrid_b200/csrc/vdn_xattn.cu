@@ -348,6 +348,13 @@ __global__ void __launch_bounds__(kThr) k_xattn_dkv(const XDims d, const XArgs a
       __syncthreads();
       acc_tile<D>(ok, sP, sQr, ty, tx);
     }
+  // selected, not left to the weights of zero: 0 times a NaN or an infinity of dO is no zero
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (4 * ty + i >= nk) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) ok[i][j] = ov[i][j] = 0.f;
+    }
   const float fk[4] = {d.scale, d.scale, d.scale, d.scale}, fv[4] = {1.f, 1.f, 1.f, 1.f};
   const long long krow = ((long long)b * d.L + k0) * d.Hkv + hk;
   if (sp.dk != nullptr) {
