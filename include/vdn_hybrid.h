@@ -549,6 +549,7 @@ typedef struct {
   int dtype;        /* vdn_dtype of q, k, q_out, k_out: VDN_F32 or VDN_BF16                   */
   int grad_dtype;   /* backward: vdn_dtype of dq_out and dk_out; VDN_F32 when dtype is         */
   float eps;        /* <= 0 selects 1e-6                                                     */
+  int zero_skipped; /* forward: 0: the output rows of a skipped token stay as they were; 1: zeros */
   long long q_stride, k_stride; /* elements from one token of q (k) to the next, so that they can be
                        slices of a packed projection; 0 = dense (H*d); else >= H*d and a
                        multiple of 16 bytes                                                  */
@@ -559,7 +560,7 @@ typedef struct {
   const float *table;     /* [table_rows, rot / 2, 2]: (cos, sin); NULL iff rot = 0            */
   const int *pos;         /* [tokens, axes] int32 in device memory.  A token with a position
                              outside [0, table_rows) on some axis is skipped: its rows of q_out and k_out stay
-                             as they were, and its gradients are zero.  NULL (axes = 1 only) =
+                             as they were (zero_skipped: zeros), and its gradients are zero.  NULL (axes = 1 only) =
                              the token's own index; then table_rows >= tokens unless rot = 0.
                              With rot = 0 and pos given, table_rows still bounds it.          */
   void *q_out, *k_out;    /* [tokens, H, d] dense; no overlap with the inputs                 */

@@ -29,6 +29,18 @@ def room_for(gigabytes):
 
 
 # ------------------------------------------------------- norm and rotation
+@pytest.mark.parametrize("case", [c for c in QK if c[0] > 8], ids=str)
+def test_qk_skipped_rows_of_new_outputs_are_zero(cuda_ok, case):
+    """Without `out` there is nothing to leave a skipped token's rows as: they are zeros, whatever the memory held."""
+    op, a, on, dt = qk_case(case, 3)
+    want = tuple(None if a[k] is None else torch.zeros(a[k].shape, device="cuda", dtype=dt) for k in "qk")
+    op(a["q"], a["k"], a["wq"], a["wk"], a["table"], a["pos"], out=want)
+    torch.cuda.synchronize()
+    stale = [torch.full(a[k].shape, math.nan, device="cuda", dtype=dt) for k in "qk" if a[k] is not None for _ in range(3)]
+    del stale  # the blocks that the call's outputs come from
+    got = op(a["q"], a["k"], a["wq"], a["wk"], a["table"], a["pos"])
+    for g, w in zip(got, want):
+        assert (g is None and w is None) or (torch.equal(g, w) and bool((g[~on] == 0).all()))
 
 
 @pytest.mark.parametrize("gdtype", ["f32", "bf16"])

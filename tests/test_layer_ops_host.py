@@ -223,3 +223,10 @@ def test_layer_wait_limit_is_bounded():
     assert L.vdn_debug_set_layer_wait_limit(2_000_000_001, check=False) == L.VDN_ERR_INVALID_ARG
     assert L.vdn_debug_set_layer_wait_limit(300) == L.VDN_OK
     assert L.vdn_debug_set_layer_wait_limit(0) == L.VDN_OK
+
+
+def test_qk_zero_skipped_is_a_flag():
+    """The output rows of skipped tokens: left, or zeros; nothing else is taken."""
+    for v in (2, -1):
+        assert L.vdn_qk_norm_rope(qk_cfg(zero_skipped=v), qk_args(), stream=0, check=False) == L.VDN_ERR_INVALID_ARG
+    assert L.vdn_qk_norm_rope_bwd_workspace_size(qk_cfg(zero_skipped=1)) == L.vdn_qk_norm_rope_bwd_workspace_size(qk_cfg()) > 0

@@ -85,7 +85,7 @@ class QkCfg(C.Structure):
     _fields_ = [("tokens", C.c_int), ("Hq", C.c_int), ("Hk", C.c_int), ("d", C.c_int), ("rot", C.c_int),
                 ("pairing", C.c_int), ("axes", C.c_int), ("sections", C.c_int * 3), ("table_rows", C.c_int),
                 ("per_head", C.c_int), ("dtype", C.c_int), ("grad_dtype", C.c_int), ("eps", C.c_float),
-                ("q_stride", C.c_longlong), ("k_stride", C.c_longlong)]
+                ("zero_skipped", C.c_int), ("q_stride", C.c_longlong), ("k_stride", C.c_longlong)]
 
 
 class QkArgs(C.Structure):

@@ -291,7 +291,8 @@ class QKNormRope(_Streamed):
     wq, wk: float32 [d] (or [H, d] with per_head), None = ones.  table: float32
     [rows, rot / 2, 2] (cos, sin), see ``rope_table``.  pos: int32 [..., axes]
     (or [...] for one axis); None = the token's index.  A token with a position
-    outside the table is skipped: its output rows are left as they were."""
+    outside the table is skipped: its output rows are zeros, or with `out` left
+    as they were."""
 
     def __init__(self, Hq: int, Hk: int, d: int, *, rot: int | None = None, pairing: str = "interleaved", sections=None,
                  per_head: bool = False, eps: float = 1e-6, device="cuda"):
@@ -307,7 +308,7 @@ class QKNormRope(_Streamed):
         self._cfgs = {}  # by sizes and strides
         self.wq_shape, self.wk_shape = ((Hq, d), (Hk, d)) if per_head else ((d,), (d,))
 
-    def _cfg_args(self, q, k, wq, wk, table, pos, grad=0):
+    def _cfg_args(self, q, k, wq, wk, table, pos, grad=0, zero_skipped=False):
         _given(q, "q")
         lead, dt, dev = q.shape[:-2], q.dtype, self.device
         qs = _head_rows(q, "q", lead, self.Hq, self.d, dt, dev)
@@ -323,17 +324,17 @@ class QKNormRope(_Streamed):
         if pos is not None:
             _need(pos, "pos", lead if self.axes == 1 and pos.dim() == len(lead) else (*lead, self.axes), torch.int32, dev)
             rows = rows or 2**31 - 1
-        key = (lead, rows, dt, grad, qs, ks)
+        key = (lead, rows, dt, grad, zero_skipped, qs, ks)
         cfg = self._cfgs.get(key)
         if cfg is None:
             cfg = self._cfgs[key] = L.QkCfg(math.prod(lead), self.Hq, self.Hk, self.d, self.rot, self.pairing, self.axes,
-                                            self.c_sections, rows, int(self.per_head), _dtype_of(q), grad, self.eps, qs, ks)
+                                            self.c_sections, rows, int(self.per_head), _dtype_of(q), grad, self.eps, int(zero_skipped), qs, ks)
         return cfg, L.QkArgs(q.data_ptr(), k.data_ptr() if self.Hk else None, L._ptr(wq), L._ptr(wk),
                              table.data_ptr() if self.rot else None, L._ptr(pos))
 
     def __call__(self, q, k, wq=None, wk=None, table=None, pos=None, out=None, stream=None):
         """(q_out, k_out), dense, of q's type; `out`: a pair of tensors to write."""
-        cfg, args = self._cfg_args(q, k, wq, wk, table, pos)
+        cfg, args = self._cfg_args(q, k, wq, wk, table, pos, zero_skipped=out is None)
         if out is None:
             out = (self._new(q.shape, q.dtype, stream), self._new(k.shape, q.dtype, stream) if self.Hk else None)
         else:

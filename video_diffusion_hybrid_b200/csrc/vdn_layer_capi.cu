@@ -37,7 +37,7 @@ vdn_status check_qk(const vdn_qk_cfg* c) {
     pairs += c->sections[i];
   }
   if (pairs != c->rot / 2) return VDN_ERR_INVALID_ARG;
-  if (c->per_head != 0 && c->per_head != 1) return VDN_ERR_INVALID_ARG;
+  if ((c->per_head != 0 && c->per_head != 1) || (c->zero_skipped != 0 && c->zero_skipped != 1)) return VDN_ERR_INVALID_ARG;
   if (!float_type(c->dtype) || !float_type(c->grad_dtype)) return VDN_ERR_INVALID_ARG;
   if (!(c->eps == c->eps)) return VDN_ERR_INVALID_ARG;
   if (!stride_ok(c->q_stride, (long long)c->Hq * c->d, c->dtype) ||
