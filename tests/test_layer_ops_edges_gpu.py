@@ -111,6 +111,20 @@ def test_cross_attn_no_gradient_past_the_length_of_a_bad_row(cuda_ok, case):
             assert m == 0 or not bool(torch.isfinite(got[key][b, :m]).all())
 
 
+def test_cross_attn_log_sum_exp_of_each_forward(cuda_ok):
+    """Two forwards before the first backward (micro-batches): each call's log-sum-exp stays its own."""
+    op, q, k, v, n, _, dt = x_case(X[9], 95)
+    q2, dy = rnd(gen(96), *q.shape, dtype=dt, scale=3.0), rnd(gen(97), *q.shape, dtype=dt)
+    y = op(q, k, v, n)
+    lse = op.lse
+    kept = lse.clone()
+    want = op.backward(q, k, v, y, lse, dy, n)
+    op(q2, k, v, n)
+    assert torch.equal(lse, kept) and not torch.equal(op.lse, kept)
+    got = op.backward(q, k, v, y, lse, dy, n)
+    assert all(torch.equal(want[key], got[key]) for key in want)
+
+
 def test_cross_attn_backward_offsets_past_31_bits(cuda_ok):
     """More than 2^31 elements of q: the last rows' dq like that of the rows alone; the other rows have no gradient, so dk
     and dv are the last rows' too, up to the order of their sums (a step of bf16 in the 2-norm)."""

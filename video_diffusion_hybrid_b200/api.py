@@ -377,8 +377,8 @@ class CrossAttention(_Streamed):
     B batch elements (``vdn_cross_attn``), and its gradients.  k and v
     [B, L, Hkv, d] may be slices of a packed projection; kv_len: int32 [B] in
     device memory, None = L everywhere.  Outputs and scratch are new on every
-    call; with keep_lse the object owns the log-sum-exp, which the next forward
-    call overwrites."""
+    call, and so is the log-sum-exp that keep_lse asks for: `lse` is the last
+    forward's, and one that was taken from there stays that call's."""
 
     def __init__(self, B: int, Tq: int, L_: int, H: int, Hkv: int, d: int, *, dtype: str = "bf16", scale: float = 0.0,
                  keep_lse: bool = False, device="cuda"):
@@ -392,8 +392,7 @@ class CrossAttention(_Streamed):
         if self.need == 0:
             raise L.VdnError(L.VDN_ERR_INVALID_ARG, "vdn_cross_attn_workspace_size")
         self.workspace = self.bwd_workspace = None  # the last calls'
-        # the log-sum-exp of every query row, which the backward takes
-        self.lse = torch.empty((B, Tq, H), dtype=torch.float32, device=self.device) if keep_lse else None
+        self.keep_lse, self.lse = keep_lse, None  # of every query row, which the backward takes
 
     def _inputs(self, q, k, v, kv_len):
         B, _, Hkv, d = self.kv_shape
@@ -414,6 +413,7 @@ class CrossAttention(_Streamed):
         else:
             _need(out, "out", self.shape, self.torch_dtype, self.device)
         self.workspace = ws = self._new(self.need, torch.uint8, stream)
+        self.lse = self._new(self.shape[:3], torch.float32, stream) if self.keep_lse else None
         a.y, a.lse, a.workspace, a.workspace_bytes = out.data_ptr(), L._ptr(self.lse), ws.data_ptr(), self.need
         self._call("vdn_cross_attn", stream, cfg, a)
         return out
