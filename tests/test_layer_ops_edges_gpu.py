@@ -177,6 +177,21 @@ def test_linear_int8_tiles(cuda_ok, M, K, N, dtype, out):
     assert bool((room[M * N:] == 7.0).all())
 
 
+@pytest.mark.parametrize("M", [1, 4, 8, 200, 1000, 5000])
+def test_linear_int8_large_scales(cuda_ok, M):
+    """Rows of values near the type's largest against a weight that brings them back: no product on the way passes what
+    the output can hold.  And small rows against large weights."""
+    g = gen(25)
+    K, N = 256, 1040
+    for up, down in ((2.0 ** 124, 2.0 ** -40), (2.0 ** -100, 2.0 ** 110)):
+        w, ws = quantize_int8(rnd(g, N, K, scale=down))
+        x = rnd(g, M, K, scale=up)
+        codes, xs = R.quantize_int8(x)
+        y = Int8Linear(w, ws, None, out_dtype="f32")(x)
+        want = R.linear_int8(codes, xs, w, ws, None)
+        within(y, want, 8 * R.EPS * want.abs(), "out")
+
+
 def test_linear_int8_offsets_past_31_bits(cuda_ok):
     """More than 2^31 elements of x and of the output: the last rows like those rows alone."""
     room_for(40)

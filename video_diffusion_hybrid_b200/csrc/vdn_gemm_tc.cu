@@ -120,17 +120,17 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&v)[3
                                                       pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
 }
 
-// 32 columns of int32 sums to scaled values: (sum rs) col_scale + bias, columns in fours (N is a multiple of 16)
+// 32 columns of int32 sums to scaled values: sum rs col_scale + bias, columns in fours (N is a multiple of 16)
 __device__ __forceinline__ void scale_s8(float (&v)[32], const GemmArgs& g, int n, int cols, float rs) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     if (i >= cols) continue;
     const float4 w = __ldg(reinterpret_cast<const float4*>(g.col_scale + n + i));
     const float4 b = g.bias ? __ldg(reinterpret_cast<const float4*>(g.bias + n + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    v[i] = fmaf((float)__float_as_int(v[i]) * rs, w.x, b.x);
-    v[i + 1] = fmaf((float)__float_as_int(v[i + 1]) * rs, w.y, b.y);
-    v[i + 2] = fmaf((float)__float_as_int(v[i + 2]) * rs, w.z, b.z);
-    v[i + 3] = fmaf((float)__float_as_int(v[i + 3]) * rs, w.w, b.w);
+    v[i] = scaled_sum(__float_as_int(v[i]), rs, w.x, b.x);
+    v[i + 1] = scaled_sum(__float_as_int(v[i + 1]), rs, w.y, b.y);
+    v[i + 2] = scaled_sum(__float_as_int(v[i + 2]), rs, w.z, b.z);
+    v[i + 3] = scaled_sum(__float_as_int(v[i + 3]), rs, w.w, b.w);
   }
 }
 

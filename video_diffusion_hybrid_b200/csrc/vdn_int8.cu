@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kFewThreads) k_int8_few(int M, int K, int N, c
     for (int j = 0; j < NC; ++j) {
       const int s = __reduce_add_sync(0xffffffffu, acc[m][j]);
       if (lane == 0) {
-        const float r = fmaf((float)s * sx[m], __ldg(w_scale + n0 + j), bias ? __ldg(bias + n0 + j) : 0.f);
+        const float r = scaled_sum(s, sx[m], __ldg(w_scale + n0 + j), bias ? __ldg(bias + n0 + j) : 0.f);
         if constexpr (sizeof(To) == 2) out[(size_t)m * N + n0 + j] = __float2bfloat16_rn(r);
         else out[(size_t)m * N + n0 + j] = r;
       }

@@ -111,6 +111,15 @@ cudaError_t allow_smem(size_t bytes) {
 }
 // device address of the projection's status words (library-owned), or null
 uint32_t* status_of_proj();
+#ifdef __CUDACC__
+// sum * row * col + bias of the 8-bit layer, fp32.  The scale above 1 comes last (or with the bias), so that a product on
+// the way passes the type's range only where the result does: a sum of up to 2^31 times a row's scale first would be
+// infinite from 2^97 on, whatever the channel's scale.
+__device__ __forceinline__ float scaled_sum(int sum, float row, float col, float bias) {
+  const bool big = fabsf(row) > 1.f;
+  return fmaf((float)sum * (big ? col : row), big ? row : col, bias);
+}
+#endif
 // out = float(a w^T) a_scale[m] w_scale[n] + bias[n]: signed 8-bit codes a [M, K], w [N, K]; clear: its status words
 // first (else an earlier kernel of the stream has cleared them)
 vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
