@@ -63,6 +63,22 @@ def test_qk_backward_of_index_positions_and_unit_weights(cuda_ok, gdtype):
             within(got["dw" + k], dw, (n + 64) * R.EPS * terms + 1e-30, "dw" + k)
 
 
+def test_qk_tokens_next_to_31_bits(cuda_ok):
+    """2^31 - 1 tokens, the largest number: the last ones are computed like a few on their own."""
+    room_for(130)
+    T, last, g = 2 ** 31 - 1, 1000, gen(51)
+    op = QKNormRope(1, 0, 8, rot=0, sections=(0,))
+    x = torch.zeros(T, 1, 8, device="cuda", dtype=torch.bfloat16)
+    x[-last:] = rnd(g, last, 1, 8, dtype=torch.bfloat16)
+    y, _ = op(x, None)
+    assert torch.equal(y[-last:], op(x[-last:], None)[0])
+    y.zero_()
+    y[-last:] = rnd(g, last, 1, 8, dtype=torch.bfloat16)
+    a = op.backward(x, None, None, None, None, y, None)
+    b = op.backward(x[-last:], None, None, None, None, y[-last:], None)
+    assert torch.equal(a["dq"][-last:], b["dq"])
+
+
 # --------------------------------------------------------- cross-attention
 WIDE = [  # more items than SMs, so that a CTA goes on from one to the next: in the forward and dq, and mostly in dk and dv
     (3, 1500, 700, 24, 24, 64, "bf16", [700, 0, 300], True),

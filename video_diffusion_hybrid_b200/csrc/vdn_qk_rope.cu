@@ -518,7 +518,7 @@ bool plan(const vdn_qk_cfg& c, QkDev& a, int hu, int resident) {
     return false;
   qk_slots(c, hu, &a.hc, &a.tpi, &a.nch);
   a.threads = (a.hc * a.tpi * lanes_per_row(c.d) + 31) / 32 * 32;
-  const long long steps = (c.tokens + a.tpi - 1) / a.tpi;
+  const long long steps = ((long long)c.tokens + a.tpi - 1) / a.tpi;
   long long gx = (long long)resident * (kThreads / a.threads) * sms / a.nch;
   if (gx > qk_max_blocks(a.nch)) gx = qk_max_blocks(a.nch);
   if (gx < 1) gx = 1;
