@@ -221,3 +221,20 @@ def test_linear_int8_offsets_past_31_bits(cuda_ok):
     q, s = quantize_int8(x)
     qt, st = quantize_int8(x[-last:])
     assert torch.equal(q[-last:], qt) and torch.equal(s[-last:], st)
+
+
+def test_int8_rows_next_to_31_bits(cuda_ok):
+    """2^31 - 1 rows, the largest number, of 16 columns: codes and scales of the last ones, and their outputs."""
+    room_for(130)
+    g, M, last = gen(54), 2 ** 31 - 1, 1000
+    x = torch.zeros(M, 16, device="cuda", dtype=torch.bfloat16)
+    x[-last:] = rnd(g, last, 16, dtype=torch.bfloat16)
+    tail = x[-last:].clone()
+    q, s = quantize_int8(x)
+    del x
+    qt, st = quantize_int8(tail)
+    assert torch.equal(q[-last:], qt) and torch.equal(s[-last:], st)
+    w, ws = quantize_int8(rnd(g, 16, 16))
+    torch.cuda.empty_cache()
+    op = Int8Linear(w, ws)
+    assert torch.equal(op(q, s)[-last:], op(qt, st))

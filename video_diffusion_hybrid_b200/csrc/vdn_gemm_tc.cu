@@ -411,8 +411,8 @@ vdn_status launch(int M, int K, int N, const void* y, const void* w, void* out, 
     if (!make_matrix_map(&ma, y, M, K, TM) || !make_matrix_map(&mb, w, K, N, 64)) return VDN_ERR_CUDA;
   }
   g.M = M; g.N = N; g.K = K;
-  g.tiles_n = (N + TN - 1) / TN;
-  const long long tiles = (long long)((M + 2 * TM - 1) / (2 * TM)) * g.tiles_n;
+  g.tiles_n = (int)(((long long)N + TN - 1) / TN);
+  const long long tiles = ((long long)M + 2 * TM - 1) / (2 * TM) * g.tiles_n;
   if (tiles > 0x3FFFFFFFLL) return VDN_ERR_UNSUPPORTED;
   g.tiles = (int)tiles;
   g.nkb = (int)(((long long)K * (BYTE ? 1 : 2) + KBYTES - 1) / KBYTES);
@@ -468,7 +468,7 @@ vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const floa
   g.col_scale = w_scale;
   g.bias = bias;
   const bool bf = out_dtype == VDN_BF16;
-  auto tiles = [&](int tm, int tn) { return (long long)((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+  auto tiles = [&](long long tm, long long tn) { return (M + tm - 1) / tm * ((N + tn - 1) / tn); };
   // Fewer 256 x 256 tiles than CTA pairs: smaller tiles, and narrower ones still while they fit on the SMs at once.
   if (tiles(2 * TM, TN) < 74) {
     if (tiles(TM, 32) <= 148)

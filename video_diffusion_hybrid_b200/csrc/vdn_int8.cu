@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
 template <typename T>
 cudaError_t quantize(const T* x, int rows, int cols, uint2* q, float* scale, uint32_t* st, cudaStream_t s) {
   // a warp a row keeps up to 1024 columns in registers, a block a row 8192
-  if (cols <= 1024) k_quantize_rows<T, 32, 4><<<(rows + 7) / 8, 256, 0, s>>>(x, rows, cols, q, scale, st);
+  if (cols <= 1024) k_quantize_rows<T, 32, 4><<<(unsigned)((rows + 7LL) / 8), 256, 0, s>>>(x, rows, cols, q, scale, st);
   else k_quantize_rows<T, 256, 4><<<rows, 256, 0, s>>>(x, rows, cols, q, scale, st);
   return cudaGetLastError();
 }
