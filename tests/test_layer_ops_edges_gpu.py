@@ -238,3 +238,19 @@ def test_int8_rows_next_to_31_bits(cuda_ok):
     torch.cuda.empty_cache()
     op = Int8Linear(w, ws)
     assert torch.equal(op(q, s)[-last:], op(qt, st))
+
+
+def test_many_sizes_leave_no_trace(cuda_ok):
+    """A user with another number of rows on every call: the objects do not grow with the numbers seen."""
+    g = gen(26)
+    w, ws = quantize_int8(rnd(g, 32, 32))
+    lin, norm = Int8Linear(w, ws), QKNormRope(1, 0, 16, rot=0, sections=(0,))
+    kv = rnd(g, 1, 1, 64 * 2000, dtype=torch.bfloat16)
+    attn = CrossAttention(1, 1, 2, 1, 1, 64)
+    q = rnd(g, 1, 1, 1, 64, dtype=torch.bfloat16)
+    for i in range(1, 700):
+        lin(torch.zeros(i, 32, device="cuda"))
+        norm(torch.zeros(i, 1, 16, device="cuda"), None)
+        k = torch.as_strided(kv, (1, 2, 1, 64), (64 * 2000, 64 + 8 * i, 64, 1))
+        attn(q, k, k)
+    assert max(len(op._cfgs) for op in (lin, norm, attn)) <= 256

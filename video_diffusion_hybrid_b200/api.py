@@ -260,6 +260,7 @@ class _Streamed:
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._like = torch.empty(0, device=self.device)
+        self._cfgs = {}  # configurations by what changes from call to call (see _keep)
 
     def _call(self, name, stream, *args):
         """The library's function with the operator's device current, on `stream` or that device's current one."""
@@ -269,6 +270,14 @@ class _Streamed:
         st = getattr(L.lib(), name)(*args, L._stream_handle(stream))
         if st != L.VDN_OK:
             raise L.VdnError(st, name)
+
+    def _keep(self, key, value):
+        """Keeps a configuration for the next call with this key.  Their number is bounded: a user with other sizes on
+        every call forms a few again now and then."""
+        if len(self._cfgs) >= 256:
+            self._cfgs.clear()
+        self._cfgs[key] = value
+        return value
 
     def _new(self, shape, dtype, stream=None) -> torch.Tensor:
         """A tensor that belongs to the stream of the call: its memory is not
@@ -305,7 +314,6 @@ class QKNormRope(_Streamed):
             raise L.VdnError(L.VDN_ERR_INVALID_ARG, "QKNormRope")
         self.axes, self.pairing, self.eps = len(self.sections), pair[pairing], eps
         self.c_sections = (ctypes.c_int * 3)(*self.sections)
-        self._cfgs = {}  # by sizes and strides
         self.wq_shape, self.wk_shape = ((Hq, d), (Hk, d)) if per_head else ((d,), (d,))
 
     def _cfg_args(self, q, k, wq, wk, table, pos, grad=0, zero_skipped=False):
@@ -327,8 +335,9 @@ class QKNormRope(_Streamed):
         key = (lead, rows, dt, grad, zero_skipped, qs, ks)
         cfg = self._cfgs.get(key)
         if cfg is None:
-            cfg = self._cfgs[key] = L.QkCfg(math.prod(lead), self.Hq, self.Hk, self.d, self.rot, self.pairing, self.axes,
-                                            self.c_sections, rows, int(self.per_head), _dtype_of(q), grad, self.eps, int(zero_skipped), qs, ks)
+            cfg = self._keep(key, L.QkCfg(math.prod(lead), self.Hq, self.Hk, self.d, self.rot, self.pairing, self.axes,
+                                          self.c_sections, rows, int(self.per_head), _dtype_of(q), grad, self.eps,
+                                          int(zero_skipped), qs, ks))
         return cfg, L.QkArgs(q.data_ptr(), k.data_ptr() if self.Hk else None, L._ptr(wq), L._ptr(wk),
                              table.data_ptr() if self.rot else None, L._ptr(pos))
 
@@ -387,7 +396,6 @@ class CrossAttention(_Streamed):
         self.torch_dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
         self.sizes = (B, Tq, L_, H, Hkv, d, L.VDN_BF16 if dtype == "bf16" else L.VDN_F32, scale)
         self.cfg = L.XattnCfg(*self.sizes)
-        self._cfgs = {}  # by the strides of k and v
         self.need, self.bwd_need = L.vdn_cross_attn_workspace_size(self.cfg), L.vdn_cross_attn_bwd_workspace_size(self.cfg)
         if self.need == 0:
             raise L.VdnError(L.VDN_ERR_INVALID_ARG, "vdn_cross_attn_workspace_size")
@@ -403,7 +411,7 @@ class CrossAttention(_Streamed):
                _head_rows(v, "v", self.kv_shape[:2], Hkv, d, self.torch_dtype, self.device))
         cfg = self._cfgs.get(key)
         if cfg is None:
-            cfg = self._cfgs[key] = L.XattnCfg(*self.sizes, *key)
+            cfg = self._keep(key, L.XattnCfg(*self.sizes, *key))
         return cfg, L.XattnArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), L._ptr(kv_len))
 
     def __call__(self, q, k, v, kv_len=None, out=None, stream=None) -> torch.Tensor:
@@ -466,7 +474,6 @@ class Int8Linear(_Streamed):
         _need(w_scale, "w_scale", (self.N,), torch.float32, self.device)
         _need(bias, "bias", (self.N,), torch.float32, self.device)
         self.w, self.w_scale, self.bias = w, w_scale, bias
-        self._cfgs = {}  # configuration and workspace size by rows and type
         self.out_torch = {"bf16": torch.bfloat16, "f32": torch.float32}[out_dtype]
         self.out_dtype = L.VDN_BF16 if out_dtype == "bf16" else L.VDN_F32
 
@@ -480,7 +487,7 @@ class Int8Linear(_Streamed):
         found = self._cfgs.get((M, x.dtype))
         if found is None:
             cfg = L.Int8Cfg(M, self.K, self.N, L.VDN_I8 if codes else _dtype_of(x), self.out_dtype)
-            found = self._cfgs[M, x.dtype] = cfg, L.vdn_linear_int8_workspace_size(cfg)
+            found = self._keep((M, x.dtype), (cfg, L.vdn_linear_int8_workspace_size(cfg)))
         cfg, need = found
         ws = self._new(need, torch.uint8, stream) if need else None
         shape = (*x.shape[:-1], self.N)
