@@ -285,8 +285,10 @@ vdn_status vdn_debug_set_read_wait_limit(unsigned long long cycles);
 
 /* The same hook for the layer's operators (no counterpart on the pages): the
  * limit, in SM clock cycles, of every bounded wait of the cross-attention's
- * kernels on the tensor cores (vdn_cross_attn, vdn_cross_attn_bwd), in the
- * launches made from now on by this process; 0 restores the default.  A wait that runs
+ * kernels on the tensor cores (vdn_cross_attn, vdn_cross_attn_bwd) and of the
+ * 8-bit layer's where one CTA has an output tile of its own (vdn_linear_int8
+ * with fewer than 74 tiles of 256 x 256), in the launches made from now on by
+ * this process; 0 restores the default.  A wait that runs
  * out records VDN_ERR_TIMEOUT and the kernel's tag in the call's status words;
  * the CTA then stops issuing, drains what it issued and exits with its outputs
  * incomplete, and the context stays usable.  Host only: launches and captured
@@ -518,8 +520,9 @@ vdn_status vdn_quantize_fp8(const void *x, int x_dtype, size_t n, void *q, float
 vdn_status vdn_out_proj_fp8(const vdn_proj_cfg *cfg, const void *y, const void *w_t, const float *scales, void *out,
                             vdn_stream_t stream);
 
-/* Status of the last vdn_out_proj / vdn_out_proj_fp8 on the current device
- * (synchronises `stream`): VDN_OK, or VDN_ERR_TIMEOUT when a bounded wait of its
+/* Status of the last vdn_out_proj / vdn_out_proj_fp8 on the current device, or
+ * of the last vdn_linear_int8 there that runs on the tensor cores and has no
+ * status words of its own (synchronises `stream`): VDN_OK, or VDN_ERR_TIMEOUT when a bounded wait of its
  * kernel gave up (the output is then incomplete); *where (if not NULL) gets
  * VDN_TAG_PROJ or VDN_TAG_NONE.  Errors: VDN_ERR_CUDA. */
 vdn_status vdn_proj_device_status(vdn_stream_t stream, unsigned *where);
@@ -686,18 +689,29 @@ typedef struct {
   void *out;              /* [M, N] row-major, out_dtype                                       */
   void *workspace;        /* codes and scales of x, 256-byte aligned; NULL when the size is 0    */
   size_t workspace_bytes; /* >= vdn_linear_int8_workspace_size(cfg)                             */
+  unsigned *status;       /* two words in device memory (4-byte aligned) for this call's bounded waits,
+                             cleared by the call; NULL = the projection's, which all calls on the
+                             device share and clear: with calls on several streams one erases what
+                             another recorded                                                */
 } vdn_int8_args;
 
 /* Bytes of workspace (0 with VDN_I8, for few rows, and for an invalid cfg). */
 size_t vdn_linear_int8_workspace_size(const vdn_int8_cfg *cfg);
 
 /* The layer on `stream`.  Up to 8 rows: one kernel, bound by the read of the
- * weight; else on the tensor cores (tcgen05 kind::i8), whose bounded waits
- * record a timeout in the words that vdn_proj_device_status reads.  Device
+ * weight, without waits (it leaves the projection's words alone); else on the
+ * tensor cores (tcgen05 kind::i8), whose bounded waits record a timeout in
+ * args->status, or in the words that vdn_proj_device_status reads.  Device
  * pointers, 16-byte aligned (x_scale 4), no overlap of out with an input.
  * Errors: VDN_ERR_INVALID_ARG, VDN_ERR_UNSUPPORTED (more than 2^30 output
  * tiles), VDN_ERR_WORKSPACE, VDN_ERR_CUDA. */
 vdn_status vdn_linear_int8(const vdn_int8_cfg *cfg, const vdn_int8_args *args, vdn_stream_t stream);
+
+/* A call's own status words, the ones it had in args->status (synchronises
+ * `stream`, which has to be that call's): VDN_OK, or VDN_ERR_TIMEOUT with
+ * VDN_TAG_PROJ in *where (if not NULL).  Errors: VDN_ERR_INVALID_ARG (NULL),
+ * VDN_ERR_CUDA. */
+vdn_status vdn_linear_int8_device_status(const unsigned *status, vdn_stream_t stream, unsigned *where);
 
 #ifdef __cplusplus
 }

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from video_diffusion_hybrid_b200 import _lib as L
-from video_diffusion_hybrid_b200.api import CrossAttention
+from video_diffusion_hybrid_b200.api import CrossAttention, Int8Linear, quantize_int8
 from video_diffusion_hybrid_b200.build import build
 
 pytestmark = pytest.mark.gpu
@@ -76,3 +76,27 @@ def test_cross_attn_wait_runs_out(cuda_ok, d):
         gave_up(lambda: op(q, k, v, n), op.status, LIMITS, L.TAG_XATTN)
         assert torch.equal(want, op(q, k, v, n)) and torch.equal(lse, op.lse)
         assert op.status() == (L.VDN_OK, 0)
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_linear_int8_wait_runs_out_and_stays_on_record(cuda_ok, codes):
+    """The timeout of one call is still there after calls on another stream, of many rows and of few."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w, ws = quantize_int8(torch.randn(272, 1296, device="cuda", generator=g))
+    x = torch.randn(300, 1296, device="cuda", generator=g)
+    given = quantize_int8(x) if codes else (x,)
+    one, two = Int8Linear(w, ws), Int8Linear(w, ws)
+    others = [x.repeat(70, 1)[:rows] for rows in (300, 5, 20000)]  # each of the layer's kernels
+    want = one(*given)
+    torch.cuda.synchronize()
+    assert one.status() == (L.VDN_OK, 0)
+    for _ in range(3):
+        gave_up(lambda: one(*given), one.status, LIMITS[:1], L.TAG_PROJ)
+        s = torch.cuda.Stream()
+        for other in others:
+            two(other, stream=s)
+            assert two.status(s) == (L.VDN_OK, 0)
+        assert one.status() == (L.VDN_ERR_TIMEOUT, L.TAG_PROJ)
+        assert torch.equal(want, one(*given)) and one.status() == (L.VDN_OK, 0)
+        gave_up(lambda: one(*given), one.status, LIMITS, L.TAG_PROJ)
+        assert torch.equal(want, one(*given)) and one.status() == (L.VDN_OK, 0)

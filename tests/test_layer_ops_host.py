@@ -230,3 +230,10 @@ def test_qk_zero_skipped_is_a_flag():
     for v in (2, -1):
         assert L.vdn_qk_norm_rope(qk_cfg(zero_skipped=v), qk_args(), stream=0, check=False) == L.VDN_ERR_INVALID_ARG
     assert L.vdn_qk_norm_rope_bwd_workspace_size(qk_cfg(zero_skipped=1)) == L.vdn_qk_norm_rope_bwd_workspace_size(qk_cfg()) > 0
+
+
+def test_int8_status_words():
+    """A call's own status words: four-byte aligned, or none."""
+    cfg = i8_cfg()
+    assert L.vdn_linear_int8(cfg, i8_args(cfg, status=P + 2), stream=0, check=False) == L.VDN_ERR_INVALID_ARG
+    assert L.vdn_linear_int8_device_status(None, stream=0) == (L.VDN_ERR_INVALID_ARG, 0)

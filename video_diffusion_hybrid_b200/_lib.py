@@ -31,7 +31,7 @@ EXPORTED = ("vdn_hybrid_attn_workspace_size", "vdn_hybrid_workspace_layout", "vd
             "vdn_qk_norm_rope", "vdn_qk_norm_rope_bwd", "vdn_qk_norm_rope_bwd_workspace_size",
             "vdn_cross_attn", "vdn_cross_attn_bwd", "vdn_cross_attn_workspace_size",
             "vdn_cross_attn_bwd_workspace_size", "vdn_cross_attn_impl", "vdn_cross_attn_device_status",
-            "vdn_quantize_int8", "vdn_linear_int8", "vdn_linear_int8_workspace_size")
+            "vdn_quantize_int8", "vdn_linear_int8", "vdn_linear_int8_workspace_size", "vdn_linear_int8_device_status")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -125,7 +125,8 @@ class Int8Cfg(C.Structure):
 class Int8Args(C.Structure):
     """Mirror of ``vdn_int8_args``."""
     _fields_ = [("x", C.c_void_p), ("x_scale", C.c_void_p), ("w", C.c_void_p), ("w_scale", C.c_void_p),
-                ("bias", C.c_void_p), ("out", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+                ("bias", C.c_void_p), ("out", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+                ("status", C.c_void_p)]
 
 
 class VdnLayout(C.Structure):
@@ -237,8 +238,10 @@ def lib() -> C.CDLL:
             fn.argtypes = [C.POINTER(cfg)]
         L.vdn_cross_attn_impl.restype = C.c_int
         L.vdn_cross_attn_impl.argtypes = [C.POINTER(XattnCfg), C.c_int]
-        L.vdn_cross_attn_device_status.restype = C.c_int
-        L.vdn_cross_attn_device_status.argtypes = [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint)]
+        for name in ("vdn_cross_attn_device_status", "vdn_linear_int8_device_status"):
+            fn = getattr(L, name)
+            fn.restype = C.c_int
+            fn.argtypes = [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint)]
         L.vdn_quantize_int8.restype = C.c_int
         L.vdn_quantize_int8.argtypes = [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]
         L.vdn_status_string.restype = C.c_char_p
@@ -445,7 +448,7 @@ def vdn_hybrid_bwd(cfg: HybridCfg, args: VdnArgs, grads: VdnGrads, stream=None, 
 
 
 TAG_READ = 3  # VDN_TAG_READ
-TAG_XATTN, TAG_XATTN_BWD = 9, 10  # VDN_TAG_XATTN, VDN_TAG_XATTN_BWD
+TAG_PROJ, TAG_XATTN, TAG_XATTN_BWD = 8, 9, 10  # VDN_TAG_PROJ, VDN_TAG_XATTN, VDN_TAG_XATTN_BWD
 
 
 def vdn_debug_set_read_wait_limit(cycles: int, check: bool = True) -> int:
@@ -535,3 +538,11 @@ def vdn_linear_int8_workspace_size(cfg: Int8Cfg) -> int:
 def vdn_linear_int8(cfg: Int8Cfg, args: Int8Args, stream=None, check: bool = True) -> int:
     """out = (x w^T) with 8-bit codes, a scale per token and per channel, and a bias."""
     return _checked(lib().vdn_linear_int8(cfg, args, _stream_handle(stream)), "vdn_linear_int8", check)
+
+
+def vdn_linear_int8_device_status(status, stream=None) -> tuple:
+    """(status, kernel tag) of the call that had these two status words
+    (synchronises the stream)."""
+    where = C.c_uint(0)
+    st = lib().vdn_linear_int8_device_status(status, _stream_handle(stream), C.byref(where))
+    return st, int(where.value)

@@ -464,8 +464,8 @@ class Int8Linear(_Streamed):
     """A linear layer on signed 8-bit codes (``vdn_linear_int8``): w int8
     [N, K] with w_scale float32 [N] (``quantize_int8`` of the weight), bias
     float32 [N] or None.  The call quantises x [..., K] (bfloat16 or float32) by
-    rows, or takes codes (int8) with x_scale.  Outputs and scratch are new on
-    every call."""
+    rows, or takes codes (int8) with x_scale.  Outputs, scratch and status words
+    are new on every call."""
 
     def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, bias=None, *, out_dtype: str = "bf16"):
         super().__init__(w.device)
@@ -474,6 +474,7 @@ class Int8Linear(_Streamed):
         _need(w_scale, "w_scale", (self.N,), torch.float32, self.device)
         _need(bias, "bias", (self.N,), torch.float32, self.device)
         self.w, self.w_scale, self.bias = w, w_scale, bias
+        self.words = None  # the last call's status words: their tensor and offset; None: nothing in it waited
         self.out_torch = {"bf16": torch.bfloat16, "f32": torch.float32}[out_dtype]
         self.out_dtype = L.VDN_BF16 if out_dtype == "bf16" else L.VDN_F32
 
@@ -489,13 +490,22 @@ class Int8Linear(_Streamed):
             cfg = L.Int8Cfg(M, self.K, self.N, L.VDN_I8 if codes else _dtype_of(x), self.out_dtype)
             found = self._keep((M, x.dtype), (cfg, L.vdn_linear_int8_workspace_size(cfg)))
         cfg, need = found
-        ws = self._new(need, torch.uint8, stream) if need else None
+        # the status words behind the scratch; a few rows of x need neither
+        ws = self._new(need + 256, torch.uint8, stream) if need or codes else None
+        self.words = (ws, need) if ws is not None else None
         shape = (*x.shape[:-1], self.N)
         if out is None:
             out = self._new(shape, self.out_torch, stream)
         else:
             _need(out, "out", shape, self.out_torch, self.device)
         a = L.Int8Args(x.data_ptr(), L._ptr(x_scale), self.w.data_ptr(), self.w_scale.data_ptr(), L._ptr(self.bias),
-                       out.data_ptr(), L._ptr(ws), need)
+                       out.data_ptr(), L._ptr(ws), need, ws.data_ptr() + need if ws is not None else None)
         self._call("vdn_linear_int8", stream, cfg, a)
         return out
+
+    def status(self, stream=None) -> tuple:
+        """(status, kernel tag) of the last call's bounded waits; `stream`: that call's."""
+        if self.words is None:
+            return L.VDN_OK, 0
+        with torch.cuda.device(self.device):
+            return L.vdn_linear_int8_device_status(self.words[0].data_ptr() + self.words[1], stream)

@@ -35,8 +35,8 @@
 // Every load lands in the issuing CTA alone: each CTA loads its own half.
 //
 // Every wait is bounded; on expiry the CTA records VDN_ERR_TIMEOUT and
-// VDN_TAG_PROJ in the projection's status words (a library-owned device array,
-// read by vdn_proj_device_status), stops issuing, drains what it issued and
+// VDN_TAG_PROJ in the call's status words (a library-owned device array, read by
+// vdn_proj_device_status, unless the 8-bit layer's caller gives its own), stops issuing, drains what it issued and
 // leaves through the pair's final cluster barrier.
 #include <cuda_fp8.h>
 
@@ -104,6 +104,8 @@ struct GemmArgs {
   void* out;
   const float* scales;  // FP8: {s_y, s_w}
   const float *row_scale, *col_scale, *bias;  // S8: [M], [N], [N] or null
+  uint32_t* status;      // of the bounded waits
+  long long wait_limit;  // of the one-CTA tiles' waits, in clock cycles; 0: the default
 };
 
 // 32 accumulator values of one row to out (16-byte stores; `cols` valid)
@@ -152,7 +154,7 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
   const uint32_t rank = cta_rank();
   const bool lead = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const Ctl ctl{abort_flag, g_proj_status, (unsigned)VDN_TAG_PROJ};
+  const Ctl ctl{abort_flag, g.status, (unsigned)VDN_TAG_PROJ};
   auto bar = [&](int i) { return smem_u32(bars + i); };
   auto lbar = [&](int i) { return map_rank(smem_u32(bars + i), 0); };
 
@@ -317,7 +319,7 @@ k_gemm_s8_small(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Ctl ctl{abort_flag, g_proj_status, (unsigned)VDN_TAG_PROJ, 0};
+  const Ctl ctl{abort_flag, g.status, (unsigned)VDN_TAG_PROJ, g.wait_limit};
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int m0 = (int)(blockIdx.x / g.tiles_n) * TM, n0 = (int)(blockIdx.x % g.tiles_n) * TNS;
   if (threadIdx.x == 0) {
@@ -441,8 +443,7 @@ vdn_status launch(int M, int K, int N, const void* y, const void* w, void* out, 
   return cudaGetLastError() == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
 
-bool clear_status(cudaStream_t s) {
-  uint32_t* st = status_of_proj();
+bool clear_status(uint32_t* st, cudaStream_t s) {
   return encode_fn() && st && cudaMemsetAsync(st, 0, sizeof(uint32_t) * 2, s) == cudaSuccess;
 }
 
@@ -450,8 +451,9 @@ bool clear_status(cudaStream_t s) {
 
 vdn_status out_proj(int M, int K, int N, int out_dtype, const void* y, const void* w, void* out, cudaStream_t s,
                     const float* scales) {
-  if (!clear_status(s)) return VDN_ERR_CUDA;
   GemmArgs g{};
+  g.status = status_of_proj();
+  if (!clear_status(g.status, s)) return VDN_ERR_CUDA;
   g.scales = scales;
   if (scales)
     return out_dtype == VDN_BF16 ? launch<K_FP8, __nv_bfloat16>(M, K, N, y, w, out, s, g)
@@ -461,9 +463,12 @@ vdn_status out_proj(int M, int K, int N, int out_dtype, const void* y, const voi
 }
 
 vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
-                   const float* w_scale, const float* bias, void* out, bool clear, cudaStream_t s) {
-  if (clear ? !clear_status(s) : !encode_fn()) return VDN_ERR_CUDA;
+                   const float* w_scale, const float* bias, void* out, uint32_t* status, bool clear, long long wait_limit,
+                   cudaStream_t s) {
+  if (clear ? !clear_status(status, s) : !encode_fn()) return VDN_ERR_CUDA;
   GemmArgs g{};
+  g.status = status;
+  g.wait_limit = wait_limit;
   g.row_scale = a_scale;
   g.col_scale = w_scale;
   g.bias = bias;

@@ -120,10 +120,11 @@ __device__ __forceinline__ float scaled_sum(int sum, float row, float col, float
   return fmaf((float)sum * (big ? col : row), big ? row : col, bias);
 }
 #endif
-// out = float(a w^T) a_scale[m] w_scale[n] + bias[n]: signed 8-bit codes a [M, K], w [N, K]; clear: its status words
-// first (else an earlier kernel of the stream has cleared them)
+// out = float(a w^T) a_scale[m] w_scale[n] + bias[n]: signed 8-bit codes a [M, K], w [N, K]; clear: the status words
+// first (else an earlier kernel of the call has cleared them)
 vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
-                   const float* w_scale, const float* bias, void* out, bool clear, cudaStream_t s);
+                   const float* w_scale, const float* bias, void* out, uint32_t* status, bool clear, long long wait_limit,
+                   cudaStream_t s);
 // codes and scale of every row of x (vdn_int8.cu); clears the two status words unless null
 cudaError_t launch_quantize_int8(const void* x, int dtype, int rows, int cols, void* q, float* scale, uint32_t* status,
                                  cudaStream_t s);

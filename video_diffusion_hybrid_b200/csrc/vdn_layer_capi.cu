@@ -119,6 +119,17 @@ size_t int8_scratch(const vdn_int8_cfg& c) {
   return up((size_t)c.M * c.K) + up((size_t)c.M * sizeof(float));
 }
 
+// a call's two status words, on the host
+vdn_status read_status(const void* words, vdn_stream_t stream, unsigned* where) {
+  if (!words) return VDN_ERR_INVALID_ARG;
+  uint32_t host[2] = {0, 0};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cudaMemcpyAsync(host, words, sizeof(host), cudaMemcpyDeviceToHost, s) != cudaSuccess) return VDN_ERR_CUDA;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return VDN_ERR_CUDA;
+  if (where) *where = host[1];
+  return host[0] ? VDN_ERR_TIMEOUT : VDN_OK;
+}
+
 }  // namespace
 }  // namespace vdn
 
@@ -195,13 +206,7 @@ vdn_status vdn_cross_attn_bwd(const vdn_xattn_cfg* cfg, const vdn_xattn_args* ar
 }
 
 vdn_status vdn_cross_attn_device_status(const void* workspace, vdn_stream_t stream, unsigned* where) {
-  if (!workspace) return VDN_ERR_INVALID_ARG;
-  uint32_t host[2] = {0, 0};
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemcpyAsync(host, workspace, sizeof(host), cudaMemcpyDeviceToHost, s) != cudaSuccess) return VDN_ERR_CUDA;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return VDN_ERR_CUDA;
-  if (where) *where = host[1];
-  return host[0] ? VDN_ERR_TIMEOUT : VDN_OK;
+  return read_status(workspace, stream, where);
 }
 
 vdn_status vdn_debug_set_layer_wait_limit(unsigned long long cycles) {
@@ -223,7 +228,7 @@ vdn_status vdn_linear_int8(const vdn_int8_cfg* cfg, const vdn_int8_args* args, v
   vdn_status st = check_int8(cfg);
   if (st != VDN_OK) return st;
   if (!args || !ok_ptr(args->x, 16) || !ok_ptr(args->w, 16) || !ok_ptr(args->w_scale, 16) || !ok_ptr(args->out, 16) ||
-      !aligned(args->bias, 16))
+      !aligned(args->bias, 16) || !aligned(args->status, 4))
     return VDN_ERR_INVALID_ARG;
   if (cfg->x_dtype == VDN_I8 ? !ok_ptr(args->x_scale, 4) : args->x_scale != nullptr) return VDN_ERR_INVALID_ARG;
   const size_t need = int8_scratch(*cfg);
@@ -231,18 +236,23 @@ vdn_status vdn_linear_int8(const vdn_int8_cfg* cfg, const vdn_int8_args* args, v
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (int8_few_supported(cfg->M, cfg->K, cfg->N))
     return launch_int8_few(*cfg, *args, s) == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
+  uint32_t* status = args->status ? args->status : status_of_proj();
+  if (!status) return VDN_ERR_CUDA;
   const void* codes = args->x;
   const float* scale = args->x_scale;
   if (cfg->x_dtype != VDN_I8) {
     char* ws = static_cast<char*>(args->workspace);
     float* sc = reinterpret_cast<float*>(ws + up((size_t)cfg->M * cfg->K));
-    uint32_t* status = status_of_proj();
-    if (!status || launch_quantize_int8(args->x, cfg->x_dtype, cfg->M, cfg->K, ws, sc, status, s) != cudaSuccess) return VDN_ERR_CUDA;
+    if (launch_quantize_int8(args->x, cfg->x_dtype, cfg->M, cfg->K, ws, sc, status, s) != cudaSuccess) return VDN_ERR_CUDA;
     codes = ws;
     scale = sc;
   }
   return gemm_s8(cfg->M, cfg->K, cfg->N, cfg->out_dtype, codes, scale, args->w, args->w_scale, args->bias, args->out,
-                 cfg->x_dtype == VDN_I8, s);
+                 status, cfg->x_dtype == VDN_I8, g_wait_limit.load(std::memory_order_relaxed), s);
+}
+
+vdn_status vdn_linear_int8_device_status(const unsigned* status, vdn_stream_t stream, unsigned* where) {
+  return read_status(status, stream, where);
 }
 
 }  // extern "C"
