@@ -435,8 +435,8 @@ size_t xattn_simt_bwd_scratch(const XDims& d) {
 cudaError_t launch_xattn_simt(const XDims& d, const XArgs& a, bool bf16, cudaStream_t s) {
   switch (d.d) {
     case 32: return bf16 ? fwd<__nv_bfloat16, 32>(d, a, s) : fwd<float, 32>(d, a, s);
-    case 64: return bf16 ? fwd<__nv_bfloat16, 64>(d, a, s) : fwd<float, 64>(d, a, s);
-    case 128: return bf16 ? fwd<__nv_bfloat16, 128>(d, a, s) : fwd<float, 128>(d, a, s);
+    case 64: return bf16 ? cudaErrorInvalidValue : fwd<float, 64>(d, a, s);
+    case 128: return bf16 ? cudaErrorInvalidValue : fwd<float, 128>(d, a, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -444,8 +444,8 @@ cudaError_t launch_xattn_simt(const XDims& d, const XArgs& a, bool bf16, cudaStr
 cudaError_t launch_xattn_simt_bwd(const XDims& d, const XArgs& a, bool bf16, cudaStream_t s) {
   switch (d.d) {
     case 32: return bf16 ? bwd<__nv_bfloat16, 32>(d, a, s) : bwd<float, 32>(d, a, s);
-    case 64: return bf16 ? bwd<__nv_bfloat16, 64>(d, a, s) : bwd<float, 64>(d, a, s);
-    case 128: return bf16 ? bwd<__nv_bfloat16, 128>(d, a, s) : bwd<float, 128>(d, a, s);
+    case 64: return bf16 ? cudaErrorInvalidValue : bwd<float, 64>(d, a, s);
+    case 128: return bf16 ? cudaErrorInvalidValue : bwd<float, 128>(d, a, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -66,7 +66,7 @@ __device__ __forceinline__ void clear_status(uint32_t* status) {
   if (blockIdx.x == 0 && threadIdx.x < 2) status[threadIdx.x] = 0;
 }
 
-// SIMT, float32 arithmetic: any type, d = 32, 64 or 128 (vdn_xattn.cu)
+// SIMT, float32 arithmetic: float32 at d = 32, 64 or 128, bf16 at d = 32 (vdn_xattn.cu)
 cudaError_t launch_xattn_simt(const XDims& d, const XArgs& a, bool bf16, cudaStream_t s);
 // needs the scratch of xattn_simt_bwd_scratch: <dO, o> per query row, and partial sums
 size_t xattn_simt_bwd_scratch(const XDims& d);
