@@ -286,9 +286,9 @@ vdn_status vdn_debug_set_read_wait_limit(unsigned long long cycles);
 /* The same hook for the layer's operators (no counterpart on the pages): the
  * limit, in SM clock cycles, of every bounded wait of the cross-attention's
  * kernels on the tensor cores (vdn_cross_attn, vdn_cross_attn_bwd) and of the
- * 8-bit layer's where one CTA has an output tile of its own (vdn_linear_int8
- * with fewer than 74 tiles of 256 x 256), in the launches made from now on by
- * this process; 0 restores the default.  A wait that runs
+ * 8-bit layer's where one CTA has an output tile of its own
+ * (vdn_linear_int8_impl 32 or 64), in the launches made from now on by this
+ * process; 0 restores the default.  A wait that runs
  * out records VDN_ERR_TIMEOUT and the kernel's tag in the call's status words;
  * the CTA then stops issuing, drains what it issued and exits with its outputs
  * incomplete, and the context stays usable.  Host only: launches and captured
@@ -697,6 +697,11 @@ typedef struct {
 
 /* Bytes of workspace (0 with VDN_I8, for few rows, and for an invalid cfg). */
 size_t vdn_linear_int8_workspace_size(const vdn_int8_cfg *cfg);
+
+/* Which implementation runs: 0 = the kernel for few rows; else the columns of
+ * the tensor cores' output tiles: 32 or 64 (one CTA, 128 rows) or 256 (a CTA
+ * pair, 256 rows); -1 = an invalid cfg. */
+int vdn_linear_int8_impl(const vdn_int8_cfg *cfg);
 
 /* The layer on `stream`.  Up to 8 rows: one kernel, bound by the read of the
  * weight, without waits (it leaves the projection's words alone); else on the

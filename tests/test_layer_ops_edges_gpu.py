@@ -162,16 +162,17 @@ def test_cross_attn_backward_offsets_past_31_bits(cuda_ok):
 
 
 # ------------------------------------------------------------ 8-bit layer
-TILES = [  # the CTA-pair kernel with more tiles than pairs, with fewer; 128 x 64 tiles; 128 x 32 tiles, several
-    (5000, 208, 1040), (4999, 6160, 1040), (20000, 48, 272), (1000, 1296, 784), (700, 272, 2000), (1008, 6144, 1024), (300, 144, 1040),
-    (513, 400, 512),
+TILES = [  # M, K, N, columns of a tile: the CTA pairs with more tiles than pairs, and with fewer; one-CTA tiles, several
+    (5000, 208, 1040, 256), (4999, 6160, 1040, 256), (20000, 48, 272, 256), (1500, 400, 2032, 256), (1000, 1296, 784, 64),
+    (700, 272, 2000, 64), (1008, 6144, 1024, 64), (300, 144, 1040, 32), (513, 400, 512, 32),
 ]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "i8"])
-@pytest.mark.parametrize("M,K,N", TILES, ids=str)
-def test_linear_int8_tiles(cuda_ok, M, K, N, dtype, out):
+@pytest.mark.parametrize("M,K,N,columns", TILES, ids=str)
+def test_linear_int8_tiles(cuda_ok, M, K, N, columns, dtype, out):
+    assert L.vdn_linear_int8_impl(L.Int8Cfg(M, K, N, L.VDN_I8, L.VDN_F32)) == columns
     g = gen(24)
     w, ws = quantize_int8(rnd(g, N, K, scale=K ** -0.5))
     bias = rnd(g, N) if M % 2 else None

@@ -237,3 +237,14 @@ def test_int8_status_words():
     cfg = i8_cfg()
     assert L.vdn_linear_int8(cfg, i8_args(cfg, status=P + 2), stream=0, check=False) == L.VDN_ERR_INVALID_ARG
     assert L.vdn_linear_int8_device_status(None, stream=0) == (L.VDN_ERR_INVALID_ARG, 0)
+
+
+@pytest.mark.parametrize("M,K,N,impl", [
+    (1, 6144, 4096, 0), (8, 6144, 4096, 0), (9, 6144, 4096, 32), (5, 131056, 16, 32), (128, 6144, 4096, 32), (237, 1280, 784, 32),
+    (237, 6144, 4096, 64), (512, 6144, 4096, 64), (1008, 6144, 2048, 64), (1008, 6144, 4096, 256), (1500, 6144, 2048, 256),
+    (2016, 6144, 784, 64), (2016, 6144, 4096, 256), (90720, 6144, 4096, 256), (2**31 - 1, 16, 16, 256), (9, 16, 2**31 - 16, 256),
+])
+def test_int8_implementation(M, K, N, impl):
+    """The kernel of few rows, one-CTA tiles up to two turns of the SMs, CTA pairs."""
+    assert L.vdn_linear_int8_impl(i8_cfg(M=M, K=K, N=N)) == impl
+    assert L.vdn_linear_int8_impl(i8_cfg(M=M, K=24, N=N)) == -1

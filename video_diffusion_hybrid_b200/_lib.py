@@ -31,7 +31,8 @@ EXPORTED = ("vdn_hybrid_attn_workspace_size", "vdn_hybrid_workspace_layout", "vd
             "vdn_qk_norm_rope", "vdn_qk_norm_rope_bwd", "vdn_qk_norm_rope_bwd_workspace_size",
             "vdn_cross_attn", "vdn_cross_attn_bwd", "vdn_cross_attn_workspace_size",
             "vdn_cross_attn_bwd_workspace_size", "vdn_cross_attn_impl", "vdn_cross_attn_device_status",
-            "vdn_quantize_int8", "vdn_linear_int8", "vdn_linear_int8_workspace_size", "vdn_linear_int8_device_status")
+            "vdn_quantize_int8", "vdn_linear_int8", "vdn_linear_int8_workspace_size", "vdn_linear_int8_device_status",
+            "vdn_linear_int8_impl")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -242,6 +243,8 @@ def lib() -> C.CDLL:
             fn = getattr(L, name)
             fn.restype = C.c_int
             fn.argtypes = [C.c_void_p, C.c_void_p, C.POINTER(C.c_uint)]
+        L.vdn_linear_int8_impl.restype = C.c_int
+        L.vdn_linear_int8_impl.argtypes = [C.POINTER(Int8Cfg)]
         L.vdn_quantize_int8.restype = C.c_int
         L.vdn_quantize_int8.argtypes = [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]
         L.vdn_status_string.restype = C.c_char_p
@@ -533,6 +536,10 @@ def vdn_quantize_int8(x, x_dtype: int, rows: int, cols: int, q, scale, stream=No
 
 def vdn_linear_int8_workspace_size(cfg: Int8Cfg) -> int:
     return int(lib().vdn_linear_int8_workspace_size(cfg))
+
+
+def vdn_linear_int8_impl(cfg: Int8Cfg) -> int:
+    return int(lib().vdn_linear_int8_impl(cfg))
 
 
 def vdn_linear_int8(cfg: Int8Cfg, args: Int8Args, stream=None, check: bool = True) -> int:

@@ -292,7 +292,7 @@ k_gemm_tc(GemmArgs g, const __grid_constant__ CUtensorMap tma, const __grid_cons
 
 // ------------------------------------------------------ few output tiles --
 // The 8-bit product where the pairs' 256 x 256 tiles would leave most SMs idle:
-// 128 x TNS tiles, one for each CTA, the same stages and roles on one SM.
+// 128 x TNS tiles, one for each CTA, the same stages and roles on one SM (s8_tile has the rule and its figures).
 // Bound by the latency of its one tile (loads, K blocks, epilogue) and, with
 // few rows, by the read of the weight.
 constexpr int STS = 8;  // stages
@@ -462,6 +462,18 @@ vdn_status out_proj(int M, int K, int N, int out_dtype, const void* y, const voi
                                : launch<K_BF16, float>(M, K, N, y, w, out, s, g);
 }
 
+// Columns of the 8-bit product's tiles: 256 (CTA pairs, 256 rows), or 64 or 32 (a CTA each, 128 rows) where the large ones
+// number fewer than the 74 pairs and the small ones run in at most two turns of the 148 SMs; the narrowest ones where they
+// all run at once.  Nothing of one turn overlaps the next, and the operands come from L2 three times as often: us a call on
+// codes, 6 of them around the kernel, by 32 / 64 columns / pairs: 12.3 / 14.3 / 22.6 at 237 x 1,280 x 784,
+// 34.8 / 22.5 / 36.9 at 237 x 6,144 x 4,096, 59.4 / 36.9 / 36.9 (two turns of 64) at 1,008 x 6,144 x 2,048,
+// 98.3 / 65.5 / 38.9 (four) at 1,008 x 6,144 x 4,096, 28.7 / 22.5 / 24.6 (three) at 3,024 x 1,280 x 784.
+int s8_tile(int M, int N) {
+  auto tiles = [&](long long tm, long long tn) { return (M + tm - 1) / tm * ((N + tn - 1) / tn); };
+  if (tiles(2 * TM, TN) >= 74 || tiles(TM, 64) > 2 * 148) return TN;
+  return tiles(TM, 32) <= 148 ? 32 : 64;
+}
+
 vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
                    const float* w_scale, const float* bias, void* out, uint32_t* status, bool clear, long long wait_limit,
                    cudaStream_t s) {
@@ -473,12 +485,9 @@ vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const floa
   g.col_scale = w_scale;
   g.bias = bias;
   const bool bf = out_dtype == VDN_BF16;
-  auto tiles = [&](long long tm, long long tn) { return (M + tm - 1) / tm * ((N + tn - 1) / tn); };
-  // Fewer 256 x 256 tiles than CTA pairs: smaller tiles, and narrower ones still while they fit on the SMs at once.
-  if (tiles(2 * TM, TN) < 74) {
-    if (tiles(TM, 32) <= 148)
-      return bf ? launch_small<32, __nv_bfloat16>(M, K, N, a, w, out, s, g) : launch_small<32, float>(M, K, N, a, w, out, s, g);
-    return bf ? launch_small<64, __nv_bfloat16>(M, K, N, a, w, out, s, g) : launch_small<64, float>(M, K, N, a, w, out, s, g);
+  switch (s8_tile(M, N)) {
+    case 32: return bf ? launch_small<32, __nv_bfloat16>(M, K, N, a, w, out, s, g) : launch_small<32, float>(M, K, N, a, w, out, s, g);
+    case 64: return bf ? launch_small<64, __nv_bfloat16>(M, K, N, a, w, out, s, g) : launch_small<64, float>(M, K, N, a, w, out, s, g);
   }
   return bf ? launch<K_S8, __nv_bfloat16>(M, K, N, a, w, out, s, g) : launch<K_S8, float>(M, K, N, a, w, out, s, g);
 }

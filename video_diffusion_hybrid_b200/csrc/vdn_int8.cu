@@ -184,6 +184,8 @@ cudaError_t quantize(const T* x, int rows, int cols, uint2* q, float* scale, uin
 // small and stays in L2), which saves a launch; a warp has NC output channels
 // and walks K in steps of 512 bytes, four byte products per instruction.  Its
 // first AHEAD steps of the weight are under way while the codes are formed.
+// (The two sides meet there, us a call from bf16 rows, this kernel / the quantiser and the tensor cores: 6,144 x 4,096
+// 9.8 / 24.3 at one row, 18.2 / 25.1 at 4, 24.3 / 25.0 at 8; 1,280 x 784 3.1 / 7.5, 5.2 / 7.6, 8.2 / 7.7.)
 constexpr int kFewRows = 8;
 constexpr int NC = 2;           // channels per warp
 constexpr int AHEAD = 8;        // steps

@@ -125,6 +125,8 @@ __device__ __forceinline__ float scaled_sum(int sum, float row, float col, float
 vdn_status gemm_s8(int M, int K, int N, int out_dtype, const void* a, const float* a_scale, const void* w,
                    const float* w_scale, const float* bias, void* out, uint32_t* status, bool clear, long long wait_limit,
                    cudaStream_t s);
+// columns of that product's tiles: 32 or 64 (a CTA each), 256 (CTA pairs)
+int s8_tile(int M, int N);
 // codes and scale of every row of x (vdn_int8.cu); clears the two status words unless null
 cudaError_t launch_quantize_int8(const void* x, int dtype, int rows, int cols, void* q, float* scale, uint32_t* status,
                                  cudaStream_t s);

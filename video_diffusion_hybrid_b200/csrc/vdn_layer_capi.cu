@@ -224,6 +224,11 @@ vdn_status vdn_quantize_int8(const void* x, int x_dtype, int rows, int cols, voi
 
 size_t vdn_linear_int8_workspace_size(const vdn_int8_cfg* cfg) { return check_int8(cfg) == VDN_OK ? int8_scratch(*cfg) : 0; }
 
+int vdn_linear_int8_impl(const vdn_int8_cfg* cfg) {
+  if (check_int8(cfg) != VDN_OK) return -1;
+  return int8_few_supported(cfg->M, cfg->K, cfg->N) ? 0 : s8_tile(cfg->M, cfg->N);
+}
+
 vdn_status vdn_linear_int8(const vdn_int8_cfg* cfg, const vdn_int8_args* args, vdn_stream_t stream) {
   vdn_status st = check_int8(cfg);
   if (st != VDN_OK) return st;
