@@ -2,6 +2,7 @@
 persistent kernel on one SM, every tile shape of the 8-bit product, rows past
 2^31 elements, sizes next to 2^31, and what a call leaves in rows that it has
 nothing to compute for."""
+import gc
 import math
 
 import pytest
@@ -23,6 +24,7 @@ def built():
 
 
 def room_for(gigabytes):
+    gc.collect()  # what a refused call's traceback holds
     torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < gigabytes << 30:
         pytest.skip(f"needs {gigabytes} GB")
@@ -77,6 +79,13 @@ def test_qk_tokens_next_to_31_bits(cuda_ok):
     a = op.backward(x, None, None, None, None, y, None)
     b = op.backward(x[-last:], None, None, None, None, y[-last:], None)
     assert torch.equal(a["dq"][-last:], b["dq"])
+
+
+def test_qk_more_tokens_than_32_bits_are_refused(cuda_ok):
+    """2^32 + 5 tokens would be 5 of them in a 32-bit count."""
+    room_for(75)
+    with pytest.raises(ValueError):
+        QKNormRope(1, 0, 8, rot=0, sections=(0,))(torch.empty(2 ** 32 + 5, 1, 8, device="cuda", dtype=torch.bfloat16), None)
 
 
 # --------------------------------------------------------- cross-attention

@@ -229,6 +229,13 @@ def _need(t, name: str, shape, dtype, device) -> None:
                          f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
+def _int32(n: int, name: str) -> int:
+    """A count that the library takes as a 32-bit integer (ctypes would drop its upper bits in silence)."""
+    if n > 2**31 - 1:
+        raise ValueError(f"{name}: {n} is more than 2^31 - 1")
+    return n
+
+
 def _head_rows(t: torch.Tensor, name: str, lead: tuple, H: int, d: int, dtype, device) -> int:
     """Checks a [*lead, H, d] tensor whose head rows are dense and whose tokens
     lie one stride apart (a slice of a packed projection); returns that stride
@@ -327,7 +334,7 @@ class QKNormRope(_Streamed):
         if self.rot:
             if table is None:
                 raise ValueError("table: the rotation needs one")
-            rows = table.shape[0]
+            rows = _int32(table.shape[0], "table rows")
             _need(table, "table", (rows, self.rot // 2, 2), torch.float32, dev)
         if pos is not None:
             _need(pos, "pos", lead if self.axes == 1 and pos.dim() == len(lead) else (*lead, self.axes), torch.int32, dev)
@@ -335,7 +342,7 @@ class QKNormRope(_Streamed):
         key = (lead, rows, dt, grad, zero_skipped, qs, ks)
         cfg = self._cfgs.get(key)
         if cfg is None:
-            cfg = self._keep(key, L.QkCfg(math.prod(lead), self.Hq, self.Hk, self.d, self.rot, self.pairing, self.axes,
+            cfg = self._keep(key, L.QkCfg(_int32(math.prod(lead), "tokens"), self.Hq, self.Hk, self.d, self.rot, self.pairing, self.axes,
                                           self.c_sections, rows, int(self.per_head), _dtype_of(q), grad, self.eps,
                                           int(zero_skipped), qs, ks))
         return cfg, L.QkArgs(q.data_ptr(), k.data_ptr() if self.Hk else None, L._ptr(wq), L._ptr(wk),
@@ -454,6 +461,7 @@ def quantize_int8(x: torch.Tensor, stream=None) -> tuple:
     (``vdn_quantize_int8``); a weight [out, in] gets a scale per output channel."""
     if x.dim() != 2 or not x.is_contiguous():
         raise ValueError("quantize_int8: expected a contiguous matrix")
+    _int32(x.shape[0], "rows"), _int32(x.shape[1], "columns")
     on = _Streamed(x.device)
     q, scale = on._new(x.shape, torch.int8, stream), on._new(x.shape[:1], torch.float32, stream)
     on._call("vdn_quantize_int8", stream, x.data_ptr(), _dtype_of(x), x.shape[0], x.shape[1], q.data_ptr(), scale.data_ptr())
@@ -470,6 +478,7 @@ class Int8Linear(_Streamed):
     def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, bias=None, *, out_dtype: str = "bf16"):
         super().__init__(w.device)
         self.N, self.K = w.shape
+        _int32(self.N, "channels"), _int32(self.K, "inputs")
         _need(w, "w", (self.N, self.K), torch.int8, self.device)
         _need(w_scale, "w_scale", (self.N,), torch.float32, self.device)
         _need(bias, "bias", (self.N,), torch.float32, self.device)
@@ -487,7 +496,7 @@ class Int8Linear(_Streamed):
         _need(x_scale, "x_scale", x.shape[:-1], torch.float32, self.device)
         found = self._cfgs.get((M, x.dtype))
         if found is None:
-            cfg = L.Int8Cfg(M, self.K, self.N, L.VDN_I8 if codes else _dtype_of(x), self.out_dtype)
+            cfg = L.Int8Cfg(_int32(M, "rows"), self.K, self.N, L.VDN_I8 if codes else _dtype_of(x), self.out_dtype)
             found = self._keep((M, x.dtype), (cfg, L.vdn_linear_int8_workspace_size(cfg)))
         cfg, need = found
         # the status words behind the scratch; a few rows of x need neither
