@@ -23,11 +23,21 @@ def built():
         build()
 
 
-def room_for(gigabytes):
-    gc.collect()  # what a refused call's traceback holds
-    torch.cuda.empty_cache()
-    if torch.cuda.mem_get_info()[0] < gigabytes << 30:
-        pytest.skip(f"needs {gigabytes} GB")
+@pytest.fixture
+def room_for(cuda_ok):
+    """room_for(n) skips below n GB of free memory; what the test had goes back at its end, before anything small that
+    stays (a library's workspace) comes to lie in it."""
+    def free():
+        gc.collect()  # what a refused call's traceback holds
+        torch.cuda.empty_cache()
+
+    def need(gigabytes):
+        free()
+        if torch.cuda.mem_get_info()[0] < gigabytes << 30:
+            pytest.skip(f"needs {gigabytes} GB")
+
+    yield need
+    free()
 
 
 # ------------------------------------------------------- norm and rotation
@@ -65,7 +75,7 @@ def test_qk_backward_of_index_positions_and_unit_weights(cuda_ok, gdtype):
             within(got["dw" + k], dw, (n + 64) * R.EPS * terms + 1e-30, "dw" + k)
 
 
-def test_qk_tokens_next_to_31_bits(cuda_ok):
+def test_qk_tokens_next_to_31_bits(room_for):
     """2^31 - 1 tokens, the largest number: the last ones are computed like a few on their own."""
     room_for(130)
     T, last, g = 2 ** 31 - 1, 1000, gen(51)
@@ -81,7 +91,7 @@ def test_qk_tokens_next_to_31_bits(cuda_ok):
     assert torch.equal(a["dq"][-last:], b["dq"])
 
 
-def test_qk_more_tokens_than_32_bits_are_refused(cuda_ok):
+def test_qk_more_tokens_than_32_bits_are_refused(room_for):
     """2^32 + 5 tokens would be 5 of them in a 32-bit count."""
     room_for(75)
     with pytest.raises(ValueError):
@@ -150,7 +160,7 @@ def test_cross_attn_log_sum_exp_of_each_forward(cuda_ok):
     assert all(torch.equal(want[key], got[key]) for key in want)
 
 
-def test_cross_attn_backward_offsets_past_31_bits(cuda_ok):
+def test_cross_attn_backward_offsets_past_31_bits(room_for):
     """More than 2^31 elements of q: the last rows' dq like that of the rows alone; the other rows have no gradient, so dk
     and dv are the last rows' too, up to the order of their sums (a step of bf16 in the 2-norm)."""
     room_for(60)
@@ -218,7 +228,7 @@ def test_linear_int8_large_scales(cuda_ok, M):
         within(y, want, 8 * R.EPS * want.abs(), "out")
 
 
-def test_linear_int8_offsets_past_31_bits(cuda_ok):
+def test_linear_int8_offsets_past_31_bits(room_for):
     """More than 2^31 elements of x and of the output: the last rows like those rows alone."""
     room_for(40)
     g, M, K, last = gen(53), 360000, 6144, 300
@@ -233,7 +243,7 @@ def test_linear_int8_offsets_past_31_bits(cuda_ok):
     assert torch.equal(q[-last:], qt) and torch.equal(s[-last:], st)
 
 
-def test_int8_rows_next_to_31_bits(cuda_ok):
+def test_int8_rows_next_to_31_bits(room_for):
     """2^31 - 1 rows, the largest number, of 16 columns: codes and scales of the last ones, and their outputs."""
     room_for(130)
     g, M, last = gen(54), 2 ** 31 - 1, 1000
