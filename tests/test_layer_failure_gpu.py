@@ -100,3 +100,30 @@ def test_linear_int8_wait_runs_out_and_stays_on_record(cuda_ok, codes):
         assert torch.equal(want, one(*given)) and one.status() == (L.VDN_OK, 0)
         gave_up(lambda: one(*given), one.status, LIMITS, L.TAG_PROJ)
         assert torch.equal(want, one(*given)) and one.status() == (L.VDN_OK, 0)
+
+
+def test_status_of_a_call_on_another_stream(cuda_ok):
+    """status() without a stream waits for the call that it tells about: the words are not read before they are written
+    (here the call starts a tenth of a second late, and the memory of its words holds something else)."""
+    op, q, k, v, n, dy = attention(64)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    w, ws = quantize_int8(torch.randn(272, 1296, device="cuda", generator=g))
+    x = torch.randn(300, 1296, device="cuda", generator=g)
+    y = op(q, k, v, n)
+    lse = op.lse
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    lin = Int8Linear(w, ws)
+    for call, status in ((lambda: op(q, k, v, n, stream=s), op.status),
+                         (lambda: op.backward(q, k, v, y, lse, dy, n, stream=s), lambda: op.status(backward=True)),
+                         (lambda: lin(x, stream=s), lin.status)):
+        call()  # the stream's allocations of these sizes exist now
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            held = [torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+                    for size in (op.need, op.bwd_need, 300 * 1296 + 4096) for _ in range(2)]
+            del held
+            torch.cuda._sleep(200_000_000)
+        call()
+        assert status() == (L.VDN_OK, 0)
+        assert s.query()  # the call was waited for

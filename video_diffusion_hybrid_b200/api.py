@@ -270,13 +270,16 @@ class _Streamed:
         self._cfgs = {}  # configurations by what changes from call to call (see _keep)
 
     def _call(self, name, stream, *args):
-        """The library's function with the operator's device current, on `stream` or that device's current one."""
+        """The library's function with the operator's device current, on `stream` or that device's current one; returns
+        the stream's handle, where the call's status words can be read."""
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
                 return self._call(name, stream, *args)
-        st = getattr(L.lib(), name)(*args, L._stream_handle(stream))
+        on = L._stream_handle(stream)
+        st = getattr(L.lib(), name)(*args, on)
         if st != L.VDN_OK:
             raise L.VdnError(st, name)
+        return on
 
     def _keep(self, key, value):
         """Keeps a configuration for the next call with this key.  Their number is bounded: a user with other sizes on
@@ -407,6 +410,7 @@ class CrossAttention(_Streamed):
         if self.need == 0:
             raise L.VdnError(L.VDN_ERR_INVALID_ARG, "vdn_cross_attn_workspace_size")
         self.workspace = self.bwd_workspace = None  # the last calls'
+        self.ran_on = self.bwd_ran_on = None  # and their streams
         self.keep_lse, self.lse = keep_lse, None  # of every query row, which the backward takes
 
     def _inputs(self, q, k, v, kv_len):
@@ -430,7 +434,7 @@ class CrossAttention(_Streamed):
         self.workspace = ws = self._new(self.need, torch.uint8, stream)
         self.lse = self._new(self.shape[:3], torch.float32, stream) if self.keep_lse else None
         a.y, a.lse, a.workspace, a.workspace_bytes = out.data_ptr(), L._ptr(self.lse), ws.data_ptr(), self.need
-        self._call("vdn_cross_attn", stream, cfg, a)
+        self.ran_on = self._call("vdn_cross_attn", stream, cfg, a)
         return out
 
     def backward(self, q, k, v, y, lse, dy, kv_len=None, stream=None) -> dict:
@@ -446,14 +450,15 @@ class CrossAttention(_Streamed):
         new = lambda shape: self._new(shape, self.torch_dtype, stream)  # noqa: E731
         g = {"dq": new(self.shape), "dk": new(self.kv_shape), "dv": new(self.kv_shape)}
         gr = L.XattnGrads(dy.data_ptr(), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr())
-        self._call("vdn_cross_attn_bwd", stream, cfg, a, gr)
+        self.bwd_ran_on = self._call("vdn_cross_attn_bwd", stream, cfg, a, gr)
         return g
 
     def status(self, backward: bool = False, stream=None) -> tuple:
-        """(status, kernel tag) of the last forward (or backward) call's bounded waits."""
-        ws = self.bwd_workspace if backward else self.workspace
+        """(status, kernel tag) of the last forward (or backward) call's bounded waits, read behind that call on its
+        stream (or on `stream`)."""
+        ws, on = (self.bwd_workspace, self.bwd_ran_on) if backward else (self.workspace, self.ran_on)
         with torch.cuda.device(self.device):
-            return L.vdn_cross_attn_device_status(ws, stream)
+            return L.vdn_cross_attn_device_status(ws, on if stream is None else stream)
 
 
 def quantize_int8(x: torch.Tensor, stream=None) -> tuple:
@@ -483,7 +488,7 @@ class Int8Linear(_Streamed):
         _need(w_scale, "w_scale", (self.N,), torch.float32, self.device)
         _need(bias, "bias", (self.N,), torch.float32, self.device)
         self.w, self.w_scale, self.bias = w, w_scale, bias
-        self.words = None  # the last call's status words: their tensor and offset; None: nothing in it waited
+        self.words = self.ran_on = None  # the last call's status words (their tensor and offset; None: nothing waits) and stream
         self.out_torch = {"bf16": torch.bfloat16, "f32": torch.float32}[out_dtype]
         self.out_dtype = L.VDN_BF16 if out_dtype == "bf16" else L.VDN_F32
 
@@ -509,12 +514,12 @@ class Int8Linear(_Streamed):
             _need(out, "out", shape, self.out_torch, self.device)
         a = L.Int8Args(x.data_ptr(), L._ptr(x_scale), self.w.data_ptr(), self.w_scale.data_ptr(), L._ptr(self.bias),
                        out.data_ptr(), L._ptr(ws), need, ws.data_ptr() + need if ws is not None else None)
-        self._call("vdn_linear_int8", stream, cfg, a)
+        self.ran_on = self._call("vdn_linear_int8", stream, cfg, a)
         return out
 
     def status(self, stream=None) -> tuple:
-        """(status, kernel tag) of the last call's bounded waits; `stream`: that call's."""
+        """(status, kernel tag) of the last call's bounded waits, read behind that call on its stream (or on `stream`)."""
         if self.words is None:
             return L.VDN_OK, 0
         with torch.cuda.device(self.device):
-            return L.vdn_linear_int8_device_status(self.words[0].data_ptr() + self.words[1], stream)
+            return L.vdn_linear_int8_device_status(self.words[0].data_ptr() + self.words[1], self.ran_on if stream is None else stream)
