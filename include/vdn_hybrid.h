@@ -590,8 +590,8 @@ size_t vdn_qk_norm_rope_bwd_workspace_size(const vdn_qk_cfg *cfg);
 
 /* The gradients of vdn_qk_norm_rope (args->q_out and k_out are not read).
  * Nothing of the forward is kept: the norm is recomputed from q and k.  The
- * weights' gradient is summed in a fixed order (the same bits on every run of
- * the same device).  Errors as vdn_qk_norm_rope; VDN_ERR_WORKSPACE. */
+ * weights' gradient is summed in fp32 in a fixed order (the same bits on every
+ * run of the same device).  Errors as vdn_qk_norm_rope; VDN_ERR_WORKSPACE. */
 vdn_status vdn_qk_norm_rope_bwd(const vdn_qk_cfg *cfg, const vdn_qk_args *args, const vdn_qk_grads *grads,
                                 vdn_stream_t stream);
 
@@ -603,7 +603,9 @@ vdn_status vdn_qk_norm_rope_bwd(const vdn_qk_cfg *cfg, const vdn_qk_args *args, 
  * log-sum-exp, and gradients.  For query head h and key head h / (H / Hkv):
  *   o = softmax(s q K^T) V over the first kv_len[b] states of batch element b;
  * with no valid state o = 0 and lse = -inf.  States past kv_len[b] are not used,
- * whatever they hold. */
+ * whatever they hold.  Scores, softmax statistics and sums in fp32; in bf16 (d =
+ * 64 and 128) the product with V takes the weights rounded to bf16 (a relative
+ * 2^-8 at most of each), their sum adds them unrounded. */
 typedef struct {
   int B, Tq;        /* batch elements, query tokens of each                              >= 1 */
   int L;            /* encoder states allocated for each batch element                   >= 1 */

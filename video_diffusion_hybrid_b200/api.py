@@ -260,7 +260,8 @@ def _head_rows(t: torch.Tensor, name: str, lead: tuple, H: int, d: int, dtype, d
 
 class _Streamed:
     """What the layer's operators share: a device of their own, and calls that
-    run with that device current."""
+    run with that device current.  Autograd does not record the calls: gradients
+    come from ``backward``.  Every call has at least one token (row)."""
 
     def __init__(self, device):
         self.device = torch.device(device)

@@ -335,9 +335,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_fwd(const QkDev a) {
     fetch(NS - 1, t + (NS - 1) * step);
     ring.wait();
     const long long oq = t * dq, ok = t * dk;
-    // A skipped token's rows, where they are to be zeros: its values masked behind the rounding (90,720 tokens of 48 heads:
-    // 452 to 461 us against 439 to 450 without; a branch that stores zeros 475, a walk of its own at the end 486, a kernel
-    // of its own 450 to 458 and 3 us more for a single token)
+    // A skipped token's rows, where they are to be zeros: its values masked behind the rounding.  90,720 tokens of 48 heads
+    // take 455 us, without it 442; predicated stores of zeros and a branch around them took 467 and 462 to 471 where this
+    // took 463, walks of their own behind or before the loop 486 and 502 to 542; a kernel of its own was as fast but 3 us
+    // more for a single token.
     const bool st = on || (a.zero_skipped && s.active && t < a.tokens);
     const uint32_t mask = on ? 0xffffffffu : 0u;
 #pragma unroll
