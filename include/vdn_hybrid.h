@@ -565,7 +565,8 @@ typedef struct {
                              outside [0, table_rows) on some axis is skipped: its rows of q_out and k_out stay
                              as they were (zero_skipped: zeros), and its gradients are zero.  NULL (axes = 1 only) =
                              the token's own index; then table_rows >= tokens unless rot = 0.
-                             With rot = 0 and pos given, table_rows still bounds it.          */
+                             With rot = 0 and pos given, table_rows still bounds it; 0 there: only
+                             tokens with a negative position are skipped.                     */
   void *q_out, *k_out;    /* [tokens, H, d] dense; no overlap with the inputs                 */
 } vdn_qk_args;
 

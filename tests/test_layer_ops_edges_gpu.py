@@ -55,6 +55,20 @@ def test_qk_skipped_rows_of_new_outputs_are_zero(cuda_ok, case):
         assert (g is None and w is None) or (torch.equal(g, w) and bool((g[~on] == 0).all()))
 
 
+@pytest.mark.parametrize("case", [(468, 24, 8, 24, 0, (0, 0, 0), "interleaved", "f32", False, False),
+                                  (36, 5, 3, 128, 0, (0,), "split", "bf16", True, True)], ids=str)
+def test_qk_norm_alone_takes_every_position(cuda_ok, case):
+    """Without a rotation there is no table: a negative position skips a token, 2^31 - 1 does not."""
+    op, a, on, dt = qk_case(case, 4)
+    assert bool((a["pos"][-1] == 2 ** 31 - 1).any()) and bool(on[-1]) and not bool(on[3])
+    out = tuple(torch.full(a[k].shape, 7.0, device="cuda", dtype=dt) for k in "qk")
+    op(a["q"], a["k"], a["wq"], a["wk"], None, a["pos"], out=out)
+    for key, t in zip("qk", out):
+        want = R.qk_norm_rope(a[key], a["w" + key], None, None, 0, case[6], op.sections, 1e-6)
+        within(t[on], want[on], R.step(dt) * want[on].abs() + 24 * R.EPS * want[on].abs().amax(-1, keepdim=True) * 2, key)
+        assert bool((t[~on] == 7.0).all())
+
+
 @pytest.mark.parametrize("gdtype", ["f32", "bf16"])
 def test_qk_backward_of_index_positions_and_unit_weights(cuda_ok, gdtype):
     for case in (QK[3], QK[2]):

@@ -310,8 +310,9 @@ class QKNormRope(_Streamed):
 
     wq, wk: float32 [d] (or [H, d] with per_head), None = ones.  table: float32
     [rows, rot / 2, 2] (cos, sin), see ``rope_table``.  pos: int32 [..., axes]
-    (or [...] for one axis); None = the token's index.  A token with a position
-    outside the table is skipped: its output rows are zeros, or with `out` left
+    (or [...] for one axis); None = the token's index (over all leading axes).
+    A token with a position outside the table (without a rotation: a negative
+    one) is skipped: its output rows are zeros, or with `out` left
     as they were."""
 
     def __init__(self, Hq: int, Hk: int, d: int, *, rot: int | None = None, pairing: str = "interleaved", sections=None,
@@ -342,7 +343,6 @@ class QKNormRope(_Streamed):
             _need(table, "table", (rows, self.rot // 2, 2), torch.float32, dev)
         if pos is not None:
             _need(pos, "pos", lead if self.axes == 1 and pos.dim() == len(lead) else (*lead, self.axes), torch.int32, dev)
-            rows = rows or 2**31 - 1
         key = (lead, rows, dt, grad, zero_skipped, qs, ks)
         cfg = self._cfgs.get(key)
         if cfg is None:

@@ -24,6 +24,8 @@
 // The weights' gradient: a block adds its threads' sums in shared memory and
 // writes them (fp32), a second kernel adds the blocks', both in a fixed order,
 // so results do not depend on timing.
+#include <climits>
+
 #include <cuda_bf16.h>
 
 #include "vdn_internal.h"
@@ -42,7 +44,7 @@ struct QkDev {
   const void *gq, *gk;    // backward: gradients of the outputs (dense)
   float* part;            // backward: partial weight gradients [gx][Hq + Hk][d], or [gx nch][2][d] for shared weights; or null
   long long tokens;
-  int Hq, Ht, d, rot, axes, rows;  // rows: table rows
+  int Hq, Ht, d, rot, axes, rows;  // rows: table rows (unsigned: 2^31 where there is no table)
   int sec0, sec01;                 // first pair of axis 1 and of axis 2
   int per_head, vec;               // vec: no lane's pairs straddle two axes
   int zero_skipped;                // forward: skipped tokens' rows are written as zeros
@@ -535,7 +537,8 @@ QkDev device_args(const vdn_qk_cfg& c, const vdn_qk_args& in) {
   a.wq = in.wq; a.wk = in.wk; a.table = in.table; a.pos = in.pos;
   a.qo = in.q_out; a.ko = in.k_out;
   a.tokens = c.tokens;
-  a.Hq = c.Hq; a.Ht = c.Hq + c.Hk; a.d = c.d; a.rot = c.rot; a.axes = c.axes; a.rows = c.table_rows;
+  a.Hq = c.Hq; a.Ht = c.Hq + c.Hk; a.d = c.d; a.rot = c.rot; a.axes = c.axes;
+  a.rows = c.rot == 0 && c.table_rows == 0 ? INT_MIN : c.table_rows;  // compared as unsigned: every position from 0 on
   a.sec0 = c.axes > 1 ? c.sections[0] : 1 << 30;
   a.sec01 = c.axes > 2 ? c.sections[0] + c.sections[1] : 1 << 30;
   const int grain = c.pairing == VDN_PAIR_SPLIT ? 8 : 4;
