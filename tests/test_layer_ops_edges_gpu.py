@@ -194,6 +194,42 @@ def test_cross_attn_backward_offsets_past_31_bits(room_for):
         assert float((x - z).norm()) <= 2 ** -8 * float(z.norm()), key
 
 
+@pytest.mark.parametrize("Tq,d,Hkv,dtype", [(1, 128, 8, "bf16"), (40, 128, 8, "bf16"), (3, 64, 16, "f32")], ids=str)
+def test_cross_attn_states_past_31_bits(room_for, Tq, d, Hkv, dtype):
+    """Packed states of more than 2^32 elements, gradients of more than 2^31.  All states but the last 700 are zeros: they
+    weigh 1 each and add nothing, so that the last 700 give the output and the gradients.  Tolerance in the 2-norm: y, P and
+    dS rounded to bf16 (a step of 2^-8 each at most, and Delta of a y rounded so), or a million fp32 sums."""
+    room_for(60)
+    g, dt, L_, last = gen(55), DT[dtype], 2 ** 20 + 77, 700
+    kv = torch.zeros(2, L_, 2, Hkv, d, device="cuda", dtype=dt)
+    kv[:, -last:] = rnd(g, 2, last, 2, Hkv, d, dtype=dt)
+    q, dy = (rnd(g, 2, Tq, Hkv, d, dtype=dt) for _ in range(2))
+    scale = 0.5
+    op = CrossAttention(2, Tq, L_, Hkv, Hkv, d, dtype=dtype, scale=scale, keep_lse=True)
+    k, v = kv[:, :, 0], kv[:, :, 1]
+    y = op(q, k, v)
+    assert op.status() == (L.VDN_OK, 0)
+    kd, vd, qd, gd = (t.double() for t in (k[:, -last:], v[:, -last:], q, dy))
+    s = scale * torch.einsum("bthd,blhd->bhtl", qd, kd)
+    top = s.amax(-1, keepdim=True).clamp_min(0)
+    z = torch.exp(s - top).sum(-1, keepdim=True) + (L_ - last) * torch.exp(-top)
+    p = torch.exp(s - top) / z
+    want = torch.einsum("bhtl,blhd->bthd", p, vd)
+    tol = 2.0 ** -6 if dtype == "bf16" else 2.0 ** -14
+    near = lambda a, b, what: float((a.double() - b).norm()) <= tol * float(b.norm()) or pytest.fail(what)  # noqa: E731
+    near(y, want, "y")
+    near(op.lse, (top + z.log()).squeeze(-1).transpose(1, 2), "lse")
+    got = op.backward(q, k, v, y, op.lse, dy)
+    assert op.status(backward=True) == (L.VDN_OK, 0)
+    ds = p * (torch.einsum("bthd,blhd->bhtl", gd, vd) - (gd * want).sum(-1).transpose(1, 2).unsqueeze(-1))
+    near(got["dq"], scale * torch.einsum("bhtl,blhd->bthd", ds, kd), "dq")
+    near(got["dk"][:, -last:], scale * torch.einsum("bhtl,bthd->blhd", ds, qd), "dk")
+    near(got["dv"][:, -last:], torch.einsum("bhtl,bthd->blhd", p, gd), "dv")
+    # a zero state's weight is exp(-lse)
+    w = torch.exp(-(top + z.log())).squeeze(-1)
+    near(got["dv"][:, 5], torch.einsum("bht,bthd->bhd", w, gd), "dv of a zero state")
+
+
 # ------------------------------------------------------------ 8-bit layer
 TILES = [  # M, K, N, columns of a tile: the CTA pairs with more tiles than pairs, and with fewer; one-CTA tiles, several
     (5000, 208, 1040, 256), (4999, 6160, 1040, 256), (20000, 48, 272, 256), (1500, 400, 2032, 256), (1000, 1296, 784, 64),
